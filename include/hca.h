@@ -42,7 +42,9 @@
  *     and every block-table entry outside the pool; hca_check_device() then
  *     reports HCA_ERR_DEVICE_CHECK naming the kinds found.  Out-of-range
  *     entries are skipped (as empty slots) with or without the check; the
- *     check changes no result.
+ *     check changes no result.  kv_cache_append records in the same way the
+ *     rows that found no place in their cache, sparse_mqa_attend_fp4 selected
+ *     entries and entries without a row.
  *   - Every entry point that launches work opens an NVTX range named after
  *     itself for the duration of the host call (no cost without a tool).
  *   - Supported shapes: c in {64, 512}, d_idx in {32, 128}; n_heads,
@@ -329,6 +331,109 @@ int sparse_mqa_attend(const hca_bf16* q, const hca_bf16* kv, long long kv_seq_st
                       long long win_seq_stride, const int32_t* q_pos, int Tq, int mode,
                       const hca_layer_cfg* cfg, const float* sink, int rotate_out, hca_bf16* out,
                       void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * KV caches: putting rows in, reading them back, attending over 4-bit entries
+ * ([Tricks] "Heterogeneous KV Cache Layout", "Partial RoPE 和 Attention Sink",
+ * "FP4 / FP8 Quantization-Aware Training").  One descriptor serves the three
+ * stored forms and the three arrangements of rows.
+ *
+ * Forms of a row of c channels, n = c - rope_dims:
+ *   HCA_KV_BF16  codes = the row, [c] bf16; scales and rope are not used.
+ *   HCA_KV_FP8   codes [n] E4M3 bytes, scales [n/64] f32, rope [rope_dims] bf16
+ *                (as kv_fp8_quantize writes them; n a positive multiple of 64).
+ *   HCA_KV_FP4   codes [n/2] bytes, two E2M1 codes each (the even channel in the
+ *                low nibble), scales [n/32] bytes X + 127, rope [rope_dims] bf16
+ *                (the first n channels as mxfp4_quantize writes them; n a
+ *                positive multiple of 32).  A row is 366 bytes at c = 512 with
+ *                64 rotary channels.
+ * ld_codes is in bf16 elements (BF16) or bytes, ld_scales in f32 (FP8) or bytes
+ * (FP4), ld_rope in bf16 elements.  Rows of codes and of rope start on 16-byte
+ * boundaries.  c is a multiple of 8, at most 512; rope_dims a multiple of 8,
+ * at most 256.
+ *
+ * Arrangement: which row holds entry e of request r (0 <= r < n_req):
+ *   flat   block_table NULL, ring 0: row r*seq_rows + e, for e < seq_rows;
+ *   ring   block_table NULL, ring 1: row r*seq_rows + e % seq_rows;
+ *   paged  block_table [n_req][bt_stride] int32 (device): row
+ *          block_table[r][e / rows_per_block] * rows_per_block + e % rows_per_block,
+ *          for e / rows_per_block < bt_stride.
+ * An entry that this gives no row below n_rows (no room, a negative block, a
+ * block past the pool) has none: it is not written, reads as zeros, and is an
+ * empty slot to the attention.
+ * ------------------------------------------------------------------------- */
+enum { HCA_KV_BF16 = 0, HCA_KV_FP8 = 1, HCA_KV_FP4 = 2 };
+
+typedef struct {
+  int form;
+  int c, rope_dims;
+  void* codes;
+  void* scales;
+  hca_bf16* rope;
+  long long ld_codes, ld_scales, ld_rope;
+  long long n_rows;             /* rows in the arrays */
+  int n_req;
+  int ring;
+  long long seq_rows;           /* flat, ring: rows of one request */
+  const int32_t* block_table;   /* paged */
+  long long bt_stride;
+  int rows_per_block;
+} hca_kv_cache;
+
+/* kv_cache_append -- new rows x [n_rows][c] (bf16, or f32 with x_is_f32 = 1; row
+ *   stride ld_x) into a cache, normalised and rotated on the way if asked.
+ *   Request b's new rows are x[row_start[b] .. row_start[b+1]) (int32 [B+1],
+ *   device, ascending), its entries first[b], first[b] + 1, ...; row_start NULL:
+ *   one row a request (n_rows = B), as in a decode step.  Rows of x before
+ *   row_start[0] or from row_start[B] on are padding and stay out, and so do the
+ *   rows of a request with first[b] < 0.  In a ring the last seq_rows new rows of
+ *   a request stay.  No other row of the cache changes.
+ *   Entry e sits at position (e+1)*rate - 1: rate 1 for raw tokens, m or m' for
+ *   compressed entries (rms_norm_rope's convention).
+ *   gamma [c] f32 or NULL: RMSNorm with norm_eps; rotate nonzero: the last
+ *   rope_dims channels turn by their position with base rope_base.  With either,
+ *   the stored form is that of the value rounded to bf16, i.e. the cache holds
+ *   what rms_norm_rope followed by kv_fp8_quantize or mxfp4_quantize gives;
+ *   with neither, that of x.  x does not overlap the cache; two requests of one
+ *   call do not name the same row (a block shared by their tables is appended to
+ *   by one of them at most).
+ *
+ * kv_cache_gather -- rows of a cache as bf16 (code * scale, rounded once):
+ *   out[b*seq_stride_out + j*ld_out ..] for b < B <= n_req, j < n_out is request
+ *   b's entry idx[b][j] (idx [B][n_out] int32), or first[b] + j, or j with both
+ *   NULL.  A negative entry, a negative first[b] and an entry without a row give
+ *   zeros.
+ *
+ * sparse_mqa_attend_fp4 -- sparse_mqa_attend over the entries of a FP4 cache, for
+ *   decode and for several queries a request (a chunk of a prompt, speculative
+ *   tokens): for query t of request r = q_req[t] (NULL: r = t), over
+ *     U(t) = { entry s of r : s in idx[t, :], 0 <= s < N }              (idx != NULL)
+ *          | { entry s of r : (s+1)*rate - 1 <= q_pos[t], s < N }       (idx == NULL)
+ *          + the raw rows of tokens max(0, q_pos[t]-n_win+1) .. q_pos[t]  (win != NULL)
+ *   token tau of request r is row win + r*win_seq_stride + (tau % win_rows)*c:
+ *   a ring of win_rows >= n_win rows per request (n_win + queries - 1 where a
+ *   request has several queries), or a whole sequence (win_rows > every q_pos).
+ *   A query with q_pos < 0 or q_req outside [0, n_req), and one without any row,
+ *   gets zeros.  q, out [Tq, n_heads, c] bf16; sink, rotate_out as in
+ *   sparse_mqa_attend.  cfg gives c (= cache->c), n_heads (1 to 128), n_win,
+ *   scale, and with rotate_out rope_dims and rope_base; its other fields are not
+ *   read.  c is a multiple of 32; scales are 16-byte aligned and ld_scales a
+ *   multiple of 16; n_idx <= 4096.  The entries are widened on chip (exactly) and
+ *   multiplied in bf16; logits, softmax and sums are f32, and the probabilities
+ *   enter the second product rounded to bf16, as the sum they are divided by.
+ *   ws: sparse_mqa_attend_fp4_workspace(cfg, Tq, N, n_idx) bytes (n_idx = 0
+ *   without idx) for the current device; (size_t)-1 for an unsupported shape. */
+int kv_cache_append(const void* x, int x_is_f32, long long ld_x, int n_rows, const int32_t* row_start,
+                    const int32_t* first, int B, int rate, const float* gamma, float norm_eps, int rotate,
+                    float rope_base, const hca_kv_cache* cache, void* stream);
+int kv_cache_gather(const hca_kv_cache* cache, int B, int n_out, const int32_t* idx, const int32_t* first,
+                    hca_bf16* out, long long ld_out, long long seq_stride_out, void* stream);
+int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, const int32_t* idx, int n_idx,
+                          int rate, const hca_bf16* win, long long win_seq_stride, int win_rows,
+                          const int32_t* q_pos, const int32_t* q_req, int Tq, const hca_layer_cfg* cfg,
+                          const float* sink, int rotate_out, hca_bf16* out, void* ws, size_t ws_bytes,
+                          void* stream);
+size_t sparse_mqa_attend_fp4_workspace(const hca_layer_cfg* cfg, int Tq, int N, int n_idx);
 
 /* ---------------------------------------------------------------------------
  * hybrid_attn_decode -- one decode step of a CSA layer and/or an HCA layer for

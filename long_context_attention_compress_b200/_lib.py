@@ -65,6 +65,13 @@ class KvFp8(ctypes.Structure):
                 ("ld_scales", c_ll), ("ld_rope", c_ll), ("seq_rows", c_ll)]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("form", c_int), ("c", c_int), ("rope_dims", c_int), ("codes", c_void_p), ("scales", c_void_p),
+                ("rope", c_void_p), ("ld_codes", c_ll), ("ld_scales", c_ll), ("ld_rope", c_ll), ("n_rows", c_ll),
+                ("n_req", c_int), ("ring", c_int), ("seq_rows", c_ll), ("block_table", c_void_p), ("bt_stride", c_ll),
+                ("rows_per_block", c_int)]
+
+
 class PrefillArgs(ctypes.Structure):
     _fields_ = [("T", c_int), ("q_pos", c_void_p), ("cand", c_void_p), ("logits", c_void_p),
                 ("kidx_cand", c_void_p), ("bias_csa", c_void_p), ("q_idx", c_void_p), ("w_idx", c_void_p),
@@ -97,6 +104,15 @@ _indexer_fp4 = _sig("csa_indexer_topk_fp4", c_int, [c_void_p, c_void_p, c_void_p
                                                     c_void_p])
 _kv_fp8_quantize = _sig("kv_fp8_quantize", c_int, [c_void_p, c_int, c_ll, c_ll, ctypes.POINTER(LayerCfg), c_void_p,
                                                    c_ll, c_void_p, c_ll, c_void_p, c_ll, c_void_p])
+_kv_append = _sig("kv_cache_append", c_int, [c_void_p, c_int, c_ll, c_int, c_void_p, c_void_p, c_int, c_int, c_void_p,
+                                             c_float, c_int, c_float, ctypes.POINTER(KvCacheDesc), c_void_p])
+_kv_gather = _sig("kv_cache_gather", c_int, [ctypes.POINTER(KvCacheDesc), c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                             c_ll, c_ll, c_void_p])
+_mqa_fp4 = _sig("sparse_mqa_attend_fp4", c_int, [c_void_p, ctypes.POINTER(KvCacheDesc), c_int, c_void_p, c_int, c_int,
+                                                 c_void_p, c_ll, c_int, c_void_p, c_void_p, c_int,
+                                                 ctypes.POINTER(LayerCfg), c_void_p, c_int, c_void_p, c_void_p, c_size,
+                                                 c_void_p])
+_mqa_fp4_ws = _sig("sparse_mqa_attend_fp4_workspace", c_size, [ctypes.POINTER(LayerCfg), c_int, c_int, c_int])
 _indexer_fp4_ws = _sig("csa_indexer_topk_fp4_workspace", c_size, [ctypes.POINTER(LayerCfg), c_int, c_int])
 _norm_rope = _sig("rms_norm_rope", c_int, [c_void_p, c_int, c_ll, c_ll, c_int, c_int, c_void_p, c_int, c_int,
                                           c_void_p, ctypes.POINTER(LayerCfg), c_void_p, c_ll, c_ll, c_void_p])
@@ -324,6 +340,167 @@ def sparse_mqa_attend(q, kv, win, q_pos, cfg: LayerCfg, idx=None, rate=None, mod
                 _ptr(sink, F32, "sink"), 1 if rotate_out else 0, _ptr(out, BF16, "out"),
                 None if ws is None else ws.data_ptr(), nb,
                 _stream(stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------
+# KV caches in bf16, FP8 or FP4, flat, paged or rings
+# ----------------------------------------------------------------------------
+HCA_KV_BF16, HCA_KV_FP8, HCA_KV_FP4 = 0, 1, 2
+_FORMS = {"bf16": HCA_KV_BF16, "fp8": HCA_KV_FP8, "fp4": HCA_KV_FP4}
+
+
+def _same_device(device, **tensors):
+    """The kernels run on the current device's stream: every tensor has to live on that device."""
+    cur = torch.cuda.current_device()
+    for name, t in dict(tensors, cache=device).items():
+        if t is None:
+            continue
+        d = t if isinstance(t, torch.device) else t.device
+        if d.type != "cuda" or d.index != cur:
+            raise ValueError(f"{name}: on {d}, but the current device is cuda:{cur}")
+
+
+def _scratch(need: int, ws, device, stream):
+    """Workspace of `need` bytes: the caller's, or one that lives until the call's work on `stream` is done."""
+    if need == SIZE_MAX:
+        raise HcaError(-2, last_error() or "unsupported configuration (workspace query)")
+    if need == 0 or ws is not None:
+        return ws, 0 if ws is None else ws.numel() * ws.element_size()
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws, need
+
+
+class KvCache:
+    """Handle of a KV cache (hca_kv_cache in include/hca.h) over the caller's tensors, which it keeps alive.
+
+    form: "bf16", "fp8" or "fp4"; c channels a row, of which the last rope_dims stay bf16.
+    codes, scales, rope: [requests, rows, width] (flat, or rings with ring=True), or [blocks, rows_per_block, width]
+    with block_table [requests, blocks of a request] int32.  codes: bf16 rows, or uint8; scales: float32 (fp8, one per
+    64 channels) or uint8 (fp4, one per 32 channels); rope: bf16.  The last dimension is contiguous and the rows are
+    evenly spaced; a dimension wider than needed is allowed (the attention wants fp4 scales in steps of 16 bytes)."""
+
+    def __init__(self, form, c, rope_dims, codes, scales=None, rope=None, block_table=None, ring=False):
+        if form not in _FORMS:
+            raise ValueError(f"form {form!r}: one of {sorted(_FORMS)}")
+        c, rope_dims = int(c), int(rope_dims)
+        n = c - rope_dims
+        want = {"codes": (codes, BF16 if form == "bf16" else torch.uint8,
+                          c if form == "bf16" else n if form == "fp8" else n // 2)}
+        if form != "bf16":
+            want["scales"] = (scales, F32 if form == "fp8" else torch.uint8, n // (64 if form == "fp8" else 32))
+            if rope_dims:
+                want["rope"] = (rope, BF16, rope_dims)
+        self.form, self.c, self.rope_dims, self.device = form, c, rope_dims, getattr(codes, "device", None)
+        self.tensors = {k: v[0] for k, v in want.items()}
+        d = self.desc = KvCacheDesc()
+        d.form, d.c, d.rope_dims, d.ring = _FORMS[form], c, rope_dims, int(bool(ring))
+        for name, (t, dtype, width) in want.items():
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch.Tensor")
+            if not t.is_cuda or t.device != codes.device:
+                raise ValueError(f"{name}: must be a CUDA tensor on the device of codes")
+            if t.dtype != dtype:
+                raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+            if t.dim() != 3 or t.shape[:2] != codes.shape[:2] or t.shape[2] < width:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(codes.shape[:2])} rows of {width}")
+            rows = t.shape[0] * t.shape[1]
+            if rows and (t.stride(2) != 1 and t.shape[2] > 1 or
+                         t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1)):
+                raise ValueError(f"{name}: rows must be contiguous and evenly spaced, strides {t.stride()}")
+            setattr(d, name, t.data_ptr())
+            setattr(d, "ld_" + name, t.stride(1) if t.shape[1] > 1 or t.shape[0] <= 1 else t.stride(0))
+        d.n_rows = codes.shape[0] * codes.shape[1]
+        if block_table is None:
+            d.n_req, d.seq_rows = codes.shape[0], codes.shape[1]
+        else:
+            if ring:
+                raise ValueError("a paged cache is not a ring")
+            if block_table.dtype != I32 or block_table.dim() != 2 or not block_table.is_contiguous():
+                raise ValueError("block_table: a contiguous [requests, blocks] int32 tensor")
+            if block_table.device != codes.device:
+                raise ValueError("block_table: must be on the device of codes")
+            d.n_req, d.bt_stride = block_table.shape
+            d.block_table, d.rows_per_block = block_table.data_ptr(), codes.shape[1]
+        self.tensors["block_table"] = block_table
+        self.n_req = d.n_req
+
+
+def kv_cache_append(x, cache: KvCache, first, row_start=None, rate=1, gamma=None, rotate=False, norm_eps=1e-6,
+                    rope_base=10000.0, stream=None):
+    """Append rows x [n, c] (bf16 or float32) to a cache: request b's rows x[row_start[b]:row_start[b+1]] (one row a
+    request without row_start) become its entries first[b], first[b] + 1, ...; entry e is normalised with gamma [c]
+    float32 if given and, with rotate, turned by position (e+1)*rate - 1 on the way.  first, row_start: int32."""
+    if x.dtype not in (BF16, F32):
+        raise TypeError(f"x: dtype {x.dtype}")
+    if x.dim() != 2 or x.shape[1] != cache.c or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"x: shape {tuple(x.shape)}, strides {x.stride()}; expected rows of {cache.c} channels")
+    _same_device(cache.device, x=x, first=first, row_start=row_start, gamma=gamma)
+    B = first.numel()
+    if row_start is not None and row_start.numel() != B + 1:
+        raise ValueError(f"row_start: {row_start.numel()} values for {B} requests")
+    if gamma is not None and gamma.numel() != cache.c:
+        raise ValueError(f"gamma: {gamma.numel()} weights for {cache.c} channels")
+    _check(_kv_append(x.data_ptr(), 1 if x.dtype == F32 else 0, x.stride(0) if x.shape[0] > 1 else cache.c, x.shape[0],
+                      _ptr(row_start, I32, "row_start"), _ptr(first, I32, "first"), B, int(rate),
+                      _ptr(gamma, F32, "gamma"), float(norm_eps), 1 if rotate else 0, float(rope_base),
+                      ctypes.byref(cache.desc), _stream(stream)))
+
+
+def kv_cache_gather(cache: KvCache, B, n_out, idx=None, first=None, out=None, stream=None):
+    """Rows of a cache as bf16 [B, n_out, c]: request b's entries idx[b] ([B, n_out] int32; negative: a zero row), or
+    first[b] + j ([B] int32), or j."""
+    _same_device(cache.device, idx=idx, first=first, out=out)
+    if idx is not None and tuple(idx.shape) != (B, n_out):
+        raise ValueError(f"idx: shape {tuple(idx.shape)}, expected {(B, n_out)}")
+    if first is not None and first.numel() != B:
+        raise ValueError(f"first: {first.numel()} values for {B} requests")
+    if out is None:
+        out = torch.empty((B, n_out, cache.c), dtype=BF16, device=cache.device)
+    elif tuple(out.shape) != (B, n_out, cache.c):
+        raise ValueError(f"out: shape {tuple(out.shape)}, expected {(B, n_out, cache.c)}")
+    _check(_kv_gather(ctypes.byref(cache.desc), int(B), int(n_out), _ptr(idx, I32, "idx"), _ptr(first, I32, "first"),
+                      _ptr(out, BF16, "out"), cache.c, n_out * cache.c, _stream(stream)))
+    return out
+
+
+def sparse_mqa_attend_fp4_workspace(cfg: LayerCfg, Tq: int, N: int, n_idx: int = 0) -> int:
+    return int(_mqa_fp4_ws(ctypes.byref(cfg), int(Tq), int(N), int(n_idx)))
+
+
+def sparse_mqa_attend_fp4(q, cache: KvCache, N, q_pos, cfg: LayerCfg, idx=None, rate=None, win=None, q_req=None, sink=None,
+                          rotate_out=False, out=None, ws=None, stream=None):
+    """MQA of q [Tq, H, c] over the entries of an FP4 cache (N per request; selected by idx [Tq, n_idx], or all visible
+    at q_pos) plus the window rows win [requests, W, c] (token tau in row tau % W; None: no window).  q_req [Tq] int32:
+    the request of each query (None: query i belongs to request i).  Other arguments as in sparse_mqa_attend."""
+    if q.dim() != 3 or tuple(q.shape[1:]) != (cfg.n_heads, cfg.c):
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [Tq, {cfg.n_heads}, {cfg.c}]")
+    _same_device(cache.device, q=q, q_pos=q_pos, idx=idx, win=win, q_req=q_req, sink=sink, out=out, ws=ws)
+    Tq = q.shape[0]
+    for name, t in (("q_pos", q_pos), ("q_req", q_req)):
+        if t is not None and t.numel() != Tq:
+            raise ValueError(f"{name}: {t.numel()} values for {Tq} queries")
+    if idx is not None and (idx.dim() != 2 or idx.shape[0] != Tq):
+        raise ValueError(f"idx: shape {tuple(idx.shape)} for {Tq} queries")
+    if win is not None and (win.dim() != 3 or win.shape[0] < cache.n_req or win.shape[2] != cfg.c):
+        raise ValueError(f"win: shape {tuple(win.shape)}, expected [{cache.n_req}, W, {cfg.c}]")
+    if sink is not None and sink.numel() != cfg.n_heads:
+        raise ValueError(f"sink: {sink.numel()} logits for {cfg.n_heads} heads")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    n_idx = 0 if idx is None else idx.shape[1]
+    if rate is None:
+        rate = cfg.m if idx is not None else cfg.m_hca
+    ws, nb = _scratch(sparse_mqa_attend_fp4_workspace(cfg, Tq, N, n_idx), ws, q.device, stream)
+    _check(_mqa_fp4(_ptr(q, BF16, "q"), ctypes.byref(cache.desc), int(N), _ptr(idx, I32, "idx"), n_idx, int(rate),
+                    _ptr(win, BF16, "win"), 0 if win is None else win.shape[1] * win.shape[2],
+                    0 if win is None else win.shape[1], _ptr(q_pos, I32, "q_pos"), _ptr(q_req, I32, "q_req"), Tq,
+                    ctypes.byref(cfg), _ptr(sink, F32, "sink"), 1 if rotate_out else 0, _ptr(out, BF16, "out"),
+                    None if ws is None else ws.data_ptr(), nb, _stream(stream)))
     return out
 
 

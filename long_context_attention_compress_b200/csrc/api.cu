@@ -383,9 +383,12 @@ int hca_check_device(void) {
   if (w1 == 0xffffffffu || w2 == 0xffffffffu || w3 == 0xffffffffu || w4 == 0xffffffffu)
     return fail(HCA_ERR_CUDA, "hca_check_device: cannot read the device error word");
   const unsigned int w5 = read_and_clear_mqa_index_error();
-  if (w5 == 0xffffffffu) return fail(HCA_ERR_CUDA, "hca_check_device: cannot read the device error word");
-  const unsigned int w = w1 | ((w2 & 1u) << 1) | (w4 << 2);
-  const unsigned int idx_bad = (w2 >> 1) | w5;
+  const unsigned int w6 = read_and_clear_mqa_fp4_error();
+  const unsigned int w7 = read_and_clear_kv_append_error();
+  if (w5 == 0xffffffffu || w6 == 0xffffffffu || w7 == 0xffffffffu)
+    return fail(HCA_ERR_CUDA, "hca_check_device: cannot read the device error word");
+  const unsigned int w = w1 | ((w2 & 1u) << 1) | (w4 << 2) | ((w6 & 1u) << 3);
+  const unsigned int idx_bad = (w2 >> 1) | w5 | (w6 >> 1);
   if (w) return fail(HCA_ERR_DEVICE_CHECK, "hca_check_device: a kernel gave up waiting (error word 0x%x)", w);
   if (w3) return fail(HCA_ERR_DEVICE_CHECK, "hca_check_device: a top-k histogram disagreed with its scores");
   if (idx_bad)
@@ -393,6 +396,7 @@ int hca_check_device(void) {
                 (idx_bad & kIdxRange) ? "entries out of range; " : "",
                 (idx_bad & kIdxCausal) ? "entries not yet visible to their query; " : "",
                 (idx_bad & kIdxBlock) ? "block-table entries outside the pool; " : "");
+  if (w7) return fail(HCA_ERR_DEVICE_CHECK, "hca_check_device: kv_cache_append was given rows that found no place");
   return HCA_OK;
 }
 
@@ -1333,6 +1337,220 @@ int csa_indexer_topk_fp4(const hca_bf16* q_idx, const float* w_idx, const uint8_
   int ev_i = 0;
   return run_indexer_topk(reinterpret_cast<const bf16*>(q_idx), w_idx, nullptr, 0, N, q_pos, B, HCA_MODE_DECODE,
                           cfg, topk_idx, ws, as_stream(stream), nullptr, 0, ev_i, 0, &k4);
+}
+
+// ---- KV caches: append, gather, attention over FP4 entries -------------------------
+static int check_cache(const hca_kv_cache* k, const char* who) {
+  CHECK(k != nullptr, HCA_ERR_INVALID_ARG, "%s: cache null", who);
+  CHECK(k->form >= HCA_KV_BF16 && k->form <= HCA_KV_FP4, HCA_ERR_INVALID_ARG, "%s: cache form %d", who, k->form);
+  CHECK(k->c > 0 && k->rope_dims >= 0 && k->rope_dims <= k->c, HCA_ERR_INVALID_ARG, "%s: cache c=%d rope_dims=%d", who,
+        k->c, k->rope_dims);
+  CHECK(k->c % 8 == 0 && k->c <= 512 && k->rope_dims % 8 == 0 && k->rope_dims <= 256, HCA_ERR_UNSUPPORTED,
+        "%s: cache c=%d rope_dims=%d (multiples of 8, at most 512 and 256)", who, k->c, k->rope_dims);
+  const int n = k->c - k->rope_dims;
+  CHECK_PTR(k->codes, who);
+  if (k->form == HCA_KV_BF16) {
+    CHECK(k->ld_codes >= k->c && k->ld_codes % 8 == 0, HCA_ERR_INVALID_ARG, "%s: cache ld_codes %lld", who, k->ld_codes);
+  } else {
+    const int group = k->form == HCA_KV_FP8 ? 64 : 32;
+    CHECK(n > 0 && n % group == 0, HCA_ERR_UNSUPPORTED, "%s: cache c - rope_dims = %d must be a positive multiple of %d",
+          who, n, group);
+    CHECK(k->ld_codes >= (k->form == HCA_KV_FP8 ? n : n / 2) && k->ld_codes % 16 == 0 && k->ld_scales >= n / group,
+          HCA_ERR_INVALID_ARG, "%s: cache row strides (codes %lld, scales %lld)", who, k->ld_codes, k->ld_scales);
+    CHECK(k->scales != nullptr && (k->form == HCA_KV_FP4 || (reinterpret_cast<uintptr_t>(k->scales) & 3u) == 0),
+          HCA_ERR_INVALID_ARG, "%s: cache scales null or misaligned", who);
+    if (k->rope_dims) {
+      CHECK_PTR(k->rope, who);
+      CHECK(k->ld_rope >= k->rope_dims && k->ld_rope % 8 == 0, HCA_ERR_INVALID_ARG, "%s: cache ld_rope %lld", who,
+            k->ld_rope);
+    }
+  }
+  CHECK(k->n_rows >= 0 && k->n_req >= 0, HCA_ERR_INVALID_ARG, "%s: cache n_rows=%lld n_req=%d", who, k->n_rows,
+        k->n_req);
+  if (k->block_table) {
+    CHECK((reinterpret_cast<uintptr_t>(k->block_table) & 3u) == 0 && k->bt_stride >= 1 && k->rows_per_block >= 1,
+          HCA_ERR_INVALID_ARG, "%s: cache block_table misaligned, bt_stride=%lld or rows_per_block=%d", who,
+          k->bt_stride, k->rows_per_block);
+    CHECK(!k->ring, HCA_ERR_UNSUPPORTED, "%s: a paged cache is not a ring", who);
+  } else {
+    CHECK(k->seq_rows >= 1, HCA_ERR_INVALID_ARG, "%s: cache seq_rows=%lld", who, k->seq_rows);
+    CHECK(k->n_req == 0 || k->n_rows / k->n_req >= k->seq_rows, HCA_ERR_INVALID_ARG,
+          "%s: cache of %lld rows for %d requests of %lld", who, k->n_rows, k->n_req, k->seq_rows);
+  }
+  return HCA_OK;
+}
+
+static KvCache kv_cache_of(const hca_kv_cache* d) {
+  KvCache k;
+  k.form = d->form;
+  k.c = d->c;
+  k.rope_dims = d->rope_dims;
+  k.codes = d->codes;
+  k.scales = d->scales;
+  k.rope = reinterpret_cast<bf16*>(d->rope);
+  k.ld_codes = d->ld_codes;
+  k.ld_scales = d->ld_scales;
+  k.ld_rope = d->ld_rope;
+  k.n_rows = d->n_rows;
+  k.seq_rows = d->block_table ? 0 : d->seq_rows;
+  k.ring = d->ring != 0;
+  k.bt = d->block_table;
+  k.bt_stride = d->bt_stride;
+  k.rpb = d->block_table ? d->rows_per_block : 1;
+  k.n_req = d->n_req;
+  return k;
+}
+
+int kv_cache_append(const void* x, int x_is_f32, long long ld_x, int n_rows, const int32_t* row_start,
+                    const int32_t* first, int B, int rate, const float* gamma, float norm_eps, int rotate,
+                    float rope_base, const hca_kv_cache* cache, void* stream) {
+  HCA_RANGE("kv_cache_append");
+  g_err.clear();
+  const char* who = "kv_cache_append";
+  const int s = check_cache(cache, who);
+  if (s != HCA_OK) return s;
+  CHECK(n_rows >= 0 && n_rows <= (1 << 30) && B >= 0 && B <= cache->n_req && rate >= 1, HCA_ERR_INVALID_ARG,
+        "%s: n_rows=%d B=%d (cache of %d requests) rate=%d", who, n_rows, B, cache->n_req, rate);
+  CHECK(row_start || n_rows == B, HCA_ERR_INVALID_ARG, "%s: %d rows for %d requests without row_start", who, n_rows, B);
+  CHECK(ld_x >= cache->c && ld_x % (x_is_f32 ? 4 : 8) == 0, HCA_ERR_INVALID_ARG, "%s: ld_x %lld", who, ld_x);
+  CHECK(!gamma || norm_eps >= 0.f, HCA_ERR_INVALID_ARG, "%s: norm_eps must be >= 0", who);
+  CHECK(!rotate || cache->rope_dims == 0 || rope_base > 0.f, HCA_ERR_INVALID_ARG, "%s: rope_base must be positive", who);
+  if (n_rows == 0 || B == 0) return HCA_OK;
+  CHECK_PTR(x, "kv_cache_append: x");
+  CHECK(first && (reinterpret_cast<uintptr_t>(first) & 3u) == 0 && (reinterpret_cast<uintptr_t>(row_start) & 3u) == 0,
+        HCA_ERR_INVALID_ARG, "%s: first null, or first or row_start misaligned", who);
+  if (gamma) CHECK_PTR(gamma, "kv_cache_append: gamma");
+  if (injected(who)) return fail(HCA_ERR_INJECTED, "kv_cache_append: injected");
+  KvAppend a;
+  a.x = x;
+  a.x_f32 = x_is_f32 != 0;
+  a.ld_x = ld_x;
+  a.n_rows = n_rows;
+  a.row_start = row_start;
+  a.first = first;
+  a.B = B;
+  a.rate = rate;
+  a.gamma = gamma;
+  a.eps = norm_eps;
+  a.rotate = rotate != 0;
+  a.rope_base = rope_base;
+  a.check = debug_checks() ? 1 : 0;
+  CUDA_TRY(launch_kv_append(a, kv_cache_of(cache), as_stream(stream)), who);
+  return HCA_OK;
+}
+
+int kv_cache_gather(const hca_kv_cache* cache, int B, int n_out, const int32_t* idx, const int32_t* first,
+                    hca_bf16* out, long long ld_out, long long seq_stride_out, void* stream) {
+  HCA_RANGE("kv_cache_gather");
+  g_err.clear();
+  const char* who = "kv_cache_gather";
+  const int s = check_cache(cache, who);
+  if (s != HCA_OK) return s;
+  CHECK(B >= 0 && B <= cache->n_req && n_out >= 0 && (long long)B * n_out <= (1ll << 31), HCA_ERR_INVALID_ARG,
+        "%s: B=%d (cache of %d requests) n_out=%d", who, B, cache->n_req, n_out);
+  CHECK(!(idx && first), HCA_ERR_INVALID_ARG, "%s: both idx and first given", who);
+  CHECK(ld_out >= cache->c && ld_out % 8 == 0 && seq_stride_out >= 0 && seq_stride_out % 8 == 0, HCA_ERR_INVALID_ARG,
+        "%s: output strides (%lld, %lld)", who, ld_out, seq_stride_out);
+  if (B == 0 || n_out == 0) return HCA_OK;
+  CHECK_PTR(out, "kv_cache_gather: out");
+  CHECK((reinterpret_cast<uintptr_t>(idx) & 3u) == 0 && (reinterpret_cast<uintptr_t>(first) & 3u) == 0,
+        HCA_ERR_INVALID_ARG, "%s: idx or first misaligned", who);
+  if (injected(who)) return fail(HCA_ERR_INJECTED, "kv_cache_gather: injected");
+  CUDA_TRY(launch_kv_gather(kv_cache_of(cache), B, n_out, idx, first, reinterpret_cast<bf16*>(out), ld_out,
+                            seq_stride_out, as_stream(stream)),
+           who);
+  return HCA_OK;
+}
+
+// The layer fields that the attention over FP4 entries reads.
+static int check_fp4_cfg(const hca_layer_cfg* cfg, const char* who) {
+  CHECK(cfg != nullptr, HCA_ERR_INVALID_ARG, "%s: cfg null", who);
+  CHECK(cfg->c > 0 && cfg->n_heads > 0 && cfg->n_win > 0, HCA_ERR_INVALID_ARG, "%s: cfg sizes must be positive", who);
+  CHECK(cfg->scale > 0.f, HCA_ERR_INVALID_ARG, "%s: cfg scale must be positive", who);
+  CHECK(cfg->c % 32 == 0 && cfg->c <= 512 && cfg->n_heads <= 128, HCA_ERR_UNSUPPORTED,
+        "%s: cfg c=%d n_heads=%d (c a multiple of 32, at most 512; at most 128 heads)", who, cfg->c, cfg->n_heads);
+  return HCA_OK;
+}
+
+static MqaFp4Problem fp4_problem(const hca_layer_cfg* cfg, int Tq, int N, const int32_t* idx, int n_idx,
+                                 const hca_bf16* win) {
+  MqaFp4Problem p = {};
+  p.kv.c = cfg->c;
+  p.N = N;
+  p.idx = idx;
+  p.n_idx = n_idx;
+  p.win = reinterpret_cast<const bf16*>(win);
+  p.n_win = cfg->n_win;
+  p.Tq = Tq;
+  p.H = cfg->n_heads;
+  p.scale = cfg->scale;
+  return p;
+}
+
+// The plan takes a window to be there, so that the size of the workspace does not depend on it.
+static MqaPlan fp4_plan(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
+  return plan_mqa_fp4(fp4_problem(cfg, Tq, N, n_idx ? reinterpret_cast<const int32_t*>(1) : nullptr, n_idx,
+                                  reinterpret_cast<const hca_bf16*>(1)),
+                      device_sm_count());
+}
+
+size_t sparse_mqa_attend_fp4_workspace(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
+  if (check_fp4_cfg(cfg, "sparse_mqa_attend_fp4") != HCA_OK || Tq < 0 || N < 0 || n_idx < 0 || n_idx > 4096)
+    return (size_t)-1;
+  return Tq == 0 ? 0 : round256(fp4_plan(cfg, Tq, N, n_idx).ws_bytes);
+}
+
+int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, const int32_t* idx, int n_idx, int rate,
+                          const hca_bf16* win, long long win_seq_stride, int win_rows, const int32_t* q_pos,
+                          const int32_t* q_req, int Tq, const hca_layer_cfg* cfg, const float* sink, int rotate_out,
+                          hca_bf16* out, void* ws, size_t ws_bytes, void* stream) {
+  HCA_RANGE("sparse_mqa_attend_fp4");
+  g_err.clear();
+  const char* who = "sparse_mqa_attend_fp4";
+  int s = check_fp4_cfg(cfg, who);
+  if (s != HCA_OK) return s;
+  if ((s = check_cache(cache, who)) != HCA_OK) return s;
+  CHECK(cache->form == HCA_KV_FP4 && !cache->ring, HCA_ERR_UNSUPPORTED, "%s: takes a flat or paged cache in FP4 form", who);
+  CHECK(cache->c == cfg->c, HCA_ERR_INVALID_ARG, "%s: cache c=%d, cfg c=%d", who, cache->c, cfg->c);
+  CHECK(aligned16(cache->scales) && cache->ld_scales % 16 == 0, HCA_ERR_INVALID_ARG,
+        "%s: cache scales not 16-byte aligned, or ld_scales %lld not a multiple of 16", who, cache->ld_scales);
+  CHECK(Tq >= 0 && N >= 0 && rate >= 1, HCA_ERR_INVALID_ARG, "%s: Tq=%d N=%d rate=%d", who, Tq, N, rate);
+  CHECK(idx ? (n_idx > 0 && n_idx <= 4096) : n_idx == 0, HCA_ERR_INVALID_ARG, "%s: n_idx=%d", who, n_idx);
+  CHECK(q_req || Tq <= cache->n_req, HCA_ERR_INVALID_ARG, "%s: %d queries for %d requests without q_req", who, Tq,
+        cache->n_req);
+  CHECK(!win || (win_rows >= cfg->n_win && win_seq_stride >= 0 && win_seq_stride % 8 == 0 &&
+                 (cache->n_req <= 1 || win_seq_stride >= (long long)win_rows * cfg->c)),
+        HCA_ERR_INVALID_ARG, "%s: window of %d rows (n_win=%d), stride %lld", who, win_rows, cfg->n_win, win_seq_stride);
+  CHECK(!rotate_out || (cfg->rope_dims > 0 && cfg->rope_dims % 8 == 0 && cfg->rope_dims <= cfg->c &&
+                        cfg->rope_dims <= 256 && cfg->rope_base > 0.f),
+        HCA_ERR_INVALID_ARG, "%s: rotate_out with rope_dims=%d rope_base=%g", who, cfg->rope_dims, cfg->rope_base);
+  const size_t need = Tq == 0 ? 0 : round256(fp4_plan(cfg, Tq, N, idx ? n_idx : 0).ws_bytes);
+  CHECK(ws_bytes >= need, HCA_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
+  if (Tq == 0) return HCA_OK;
+  CHECK_PTR(q, "sparse_mqa_attend_fp4: q");
+  CHECK_PTR(out, "sparse_mqa_attend_fp4: out");
+  CHECK(!win || aligned16(win), HCA_ERR_INVALID_ARG, "%s: win not 16-byte aligned", who);
+  CHECK(q_pos && ((reinterpret_cast<uintptr_t>(q_pos) | reinterpret_cast<uintptr_t>(q_req) |
+                   reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(sink)) & 3u) == 0,
+        HCA_ERR_INVALID_ARG, "%s: q_pos null, or q_pos, q_req, idx or sink misaligned", who);
+  if (need) CHECK(ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0, HCA_ERR_INVALID_ARG,
+                  "%s: ws null or not 256-byte aligned", who);
+  if (injected(who)) return fail(HCA_ERR_INJECTED, "sparse_mqa_attend_fp4: injected");
+  MqaFp4Problem p = fp4_problem(cfg, Tq, N, idx, idx ? n_idx : 0, win);
+  p.q = reinterpret_cast<const bf16*>(q);
+  p.kv = kv_cache_of(cache);
+  p.rate = rate;
+  p.win_seq_stride = win_seq_stride;
+  p.win_rows = win_rows;
+  p.q_pos = q_pos;
+  p.q_req = q_req;
+  p.sink = sink;
+  p.rope_dims = rotate_out ? cfg->rope_dims : 0;
+  p.rope_base = cfg->rope_base;
+  p.out = reinterpret_cast<bf16*>(out);
+  p.check = debug_checks() ? 1 : 0;
+  CUDA_TRY(launch_mqa_fp4(p, fp4_plan(cfg, Tq, N, idx ? n_idx : 0), ws, as_stream(stream)), who);
+  return HCA_OK;
 }
 
 }  // extern "C"

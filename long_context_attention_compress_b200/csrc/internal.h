@@ -51,6 +51,59 @@ cudaError_t launch_kv_fp8_quantize(const void* x, bool x_f32, long long ld_x, lo
 cudaError_t launch_kv_fp8_gather(const KvFp8& kv, int c, int rope_dims, int B, int n_out, const int32_t* idx,
                                  int n_src, bf16* out, int32_t* idx_out, cudaStream_t stream);
 
+// ---- kv_cache.cu (rows into and out of a cache in any form) ---------------------------
+// Device form of hca_kv_cache (see hca.h).
+struct KvCache {
+  int form, c, rope_dims;
+  void* codes;
+  void* scales;
+  bf16* rope;
+  long long ld_codes, ld_scales, ld_rope;
+  long long n_rows;       // no row at or past it is touched
+  long long seq_rows;     // flat: entries a request has room for; ring: its rows
+  int ring;
+  const int32_t* bt;      // paged: request r's entry e is row bt[r*bt_stride + e/rpb]*rpb + e%rpb
+  long long bt_stride;
+  int rpb;
+  int n_req;
+};
+// Row of entry e of request `req`, or -1: an entry without room, or a block outside the pool.
+__device__ __forceinline__ long long kv_row(const KvCache& k, int req, long long e) {
+  if (e < 0 || req < 0 || req >= k.n_req) return -1;
+  long long r;
+  if (k.bt) {
+    const long long j = e / k.rpb;
+    if (j >= k.bt_stride) return -1;
+    const int blk = k.bt[req * k.bt_stride + j];
+    if (blk < 0) return -1;
+    r = (long long)blk * k.rpb + (e - j * k.rpb);
+  } else {
+    if (k.ring) e %= k.seq_rows;
+    if (e >= k.seq_rows) return -1;
+    r = req * k.seq_rows + e;
+  }
+  return r < k.n_rows ? r : -1;
+}
+struct KvAppend {
+  const void* x;
+  bool x_f32;
+  long long ld_x;
+  int n_rows;
+  const int32_t* row_start;  // [B+1] or nullptr: one row a request
+  const int32_t* first;      // [B]
+  int B, rate;
+  const float* gamma;        // or nullptr: no normalisation
+  float eps;
+  int rotate;
+  float rope_base;
+  int check;                 // record rows that found no place
+};
+cudaError_t launch_kv_append(const KvAppend& a, const KvCache& k, cudaStream_t stream);
+// out[b*seq_out + j*ld_out + :] = row of entry (idx ? idx[b*n_out + j] : first ? first[b] + j : j), zeros where none
+cudaError_t launch_kv_gather(const KvCache& k, int B, int n_out, const int32_t* idx, const int32_t* first, bf16* out,
+                             long long ld_out, long long seq_out, cudaStream_t stream);
+unsigned int read_and_clear_kv_append_error();  // nonzero: rows found no place
+
 // ---- norm_rope.cu -------------------------------------------------------------
 // Q/KV RMSNorm + partial RoPE of rows (see rms_norm_rope in hca.h for the row
 // addressing and positions).
@@ -241,6 +294,32 @@ cudaError_t launch_mqa_combine(const float* ws_o, const float2* ws_ml, int Tq, i
                                const int32_t* q_pos, int rope_dims, float rope_base,
                                cudaStream_t stream,
                                bool pdl = false);
+
+// ---- mqa_fp4.cu (attention over a cache in FP4 form) ----------------------------------
+struct MqaFp4Problem {
+  const bf16* q;            // [Tq, H, c]
+  KvCache kv;               // FP4 form
+  int N;                    // entries of every request
+  const int32_t* idx;       // [Tq, n_idx] or nullptr (every visible entry)
+  int n_idx;
+  int rate;
+  const bf16* win;          // ring of win_rows raw rows per request, or nullptr: no window
+  long long win_seq_stride;
+  int win_rows, n_win;
+  const int32_t* q_pos;
+  const int32_t* q_req;     // [Tq] or nullptr: query i belongs to request i
+  int Tq, H;
+  float scale;
+  const float* sink;
+  int rope_dims;            // > 0: the output's last rope_dims channels turn back by -q_pos
+  float rope_base;
+  bf16* out;
+  int check;
+};
+// (sizes alone decide the plan: Tq, H, c, N, n_idx and whether idx and win are given)
+MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms);
+cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, cudaStream_t stream);
+unsigned int read_and_clear_mqa_fp4_error();  // bit 0: a wait gave up; entry_check bits << 1
 
 // ---- mqa_tc.cu (tcgen05) -------------------------------------------------------------
 bool mqa_tc_supported(const MqaProblem& p);

@@ -23,45 +23,12 @@
 // layer every visible row.
 
 #include "common.cuh"
+#include "formats.cuh"
 #include "internal.h"
 
 namespace hca {
 
 namespace {
-constexpr int kFp8Group = 64;
-constexpr double kE4m3Max = 448.0;
-
-// E4M3 byte of q (f64), ties to even, saturating; sign bit 7, exponent bits 3-6
-// (bias 7, field 0 = subnormal with spacing 2^-9), mantissa bits 0-2.
-__device__ __forceinline__ uint32_t e4m3_encode(double q) {
-  const uint32_t sign = q < 0.0 ? 0x80u : 0u;
-  const double a = fabs(q);
-  if (a >= kE4m3Max) return sign | 0x7Eu;  // 1.75 * 2^8 = 448
-  int e = -6;
-  if (a > 0.0) {
-    int ex;
-    frexp(a, &ex);  // a = f * 2^ex, f in [0.5, 1): floor(log2 a) = ex - 1
-    e = ex - 1 < -6 ? -6 : ex - 1;
-  }
-  const double qq = ldexp(a, 3 - e);  // a / 2^(e-3), exact
-  double fl = floor(qq);
-  const double frac = qq - fl;
-  if (frac > 0.5 || (frac == 0.5 && fmod(fl, 2.0) == 1.0)) fl += 1.0;
-  int m = (int)fl;  // value = m * 2^(e-3), m in [0, 16]
-  if (m >= 16) {    // rounded up into the next binade
-    m = 8;
-    ++e;
-  }
-  if (m < 8) return sign | (uint32_t)m;  // subnormal (e = -6): exponent field 0
-  return sign | ((uint32_t)(e + 7) << 3) | (uint32_t)(m - 8);
-}
-
-__device__ __forceinline__ float e4m3_decode(uint32_t b) {
-  const uint32_t ex = (b >> 3) & 15u, m = b & 7u;
-  const float mag = ex ? __uint_as_float(((ex + 120u) << 23) | (m << 20)) : (float)m * 0.001953125f;  // m * 2^-9
-  return (b & 0x80u) ? -mag : mag;
-}
-
 template <bool F32>
 __device__ __forceinline__ float load_x(const void* x, long long i) {
   if constexpr (F32) return reinterpret_cast<const float*>(x)[i];
