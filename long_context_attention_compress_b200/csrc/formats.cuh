@@ -30,37 +30,64 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
 // and a mask line them up with the high bytes of those elements.  2^X is applied by one
 // bf16x2 multiply, exact while every nonzero product stays a normal bf16
 // (|X| <= 125: 0.5 * 2^X .. 6 * 2^X); beyond that the values are formed in f32 (as
-// exact) and rounded once.
-__device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, int X, uint32_t* o) {
+// exact) and rounded once.  (_normal: for |X| <= 125.)
+__device__ __forceinline__ void e2m1x8_to_bf16_normal(uint32_t w, int X, uint32_t* o) {
   constexpr uint32_t kHiLo = 0x3F3F3F00u, kHiHi = 0x40404040u, kLoLo = 0xC0800000u, kLoHi = 0xC0804000u;
-  if (X >= -125 && X <= 125) {
-    const uint32_t w4 = w << 4, wh = w >> 16;
-    // high bytes of elements 0-3 and 4-7, signs included; low bytes likewise
-    const uint32_t h0 = __byte_perm(kHiLo, kHiHi, w) | (__byte_perm(w4, w, 0x5140u) & 0x80808080u);
-    const uint32_t h1 = __byte_perm(kHiLo, kHiHi, wh) | (__byte_perm(w4, w, 0x7362u) & 0x80808080u);
-    const uint32_t l0 = __byte_perm(kLoLo, kLoHi, w), l1 = __byte_perm(kLoLo, kLoHi, wh);
-    uint32_t p[4];
-    p[0] = __byte_perm(l0, h0, 0x5140u);
-    p[1] = __byte_perm(l0, h0, 0x7362u);
-    p[2] = __byte_perm(l1, h1, 0x5140u);
-    p[3] = __byte_perm(l1, h1, 0x7362u);
-    const uint32_t sb = (uint32_t)(127 + X) << 7;  // bf16 bits of 2^X
-    const uint32_t sbits = sb | (sb << 16);
-    __nv_bfloat162 sc;
-    memcpy(&sc, &sbits, 4);
+  const uint32_t w4 = w << 4, wh = w >> 16;
+  // high bytes of elements 0-3 and 4-7, signs included; low bytes likewise
+  const uint32_t h0 = __byte_perm(kHiLo, kHiHi, w) | (__byte_perm(w4, w, 0x5140u) & 0x80808080u);
+  const uint32_t h1 = __byte_perm(kHiLo, kHiHi, wh) | (__byte_perm(w4, w, 0x7362u) & 0x80808080u);
+  const uint32_t l0 = __byte_perm(kLoLo, kLoHi, w), l1 = __byte_perm(kLoLo, kLoHi, wh);
+  uint32_t p[4];
+  p[0] = __byte_perm(l0, h0, 0x5140u);
+  p[1] = __byte_perm(l0, h0, 0x7362u);
+  p[2] = __byte_perm(l1, h1, 0x5140u);
+  p[3] = __byte_perm(l1, h1, 0x7362u);
+  const uint32_t sb = (uint32_t)(127 + X) << 7;  // bf16 bits of 2^X
+  const uint32_t sbits = sb | (sb << 16);
+  __nv_bfloat162 sc;
+  memcpy(&sc, &sbits, 4);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      __nv_bfloat162 v;
-      memcpy(&v, &p[k], 4);
-      v = __hmul2(v, sc);
-      memcpy(&o[k], &v, 4);
-    }
+  for (int k = 0; k < 4; ++k) {
+    __nv_bfloat162 v;
+    memcpy(&v, &p[k], 4);
+    v = __hmul2(v, sc);
+    memcpy(&o[k], &v, 4);
+  }
+}
+__device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, int X, uint32_t* o) {
+  if (X >= -125 && X <= 125) {
+    e2m1x8_to_bf16_normal(w, X, o);
     return;
   }
   const float scf = ldexpf(1.f, X);
 #pragma unroll
   for (int j = 0; j < 8; j += 2)
     o[j >> 1] = pack_bf16x2(e2m1_value((w >> (4 * j)) & 15u) * scf, e2m1_value((w >> (4 * j + 4)) & 15u) * scf);
+}
+
+// A whole MXFP4 block: 32 codes (16 bytes) times 2^X -> 32 bf16 as four 16-byte words; one branch for all of it, so
+// that the four words' instructions interleave.
+__device__ __forceinline__ void e2m1x32_to_bf16(const uint4& w, int X, uint4* o) {
+  const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+  uint32_t t[4];
+  if (X >= -125 && X <= 125) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e2m1x8_to_bf16_normal(c[i], X, t);
+      o[i] = make_uint4(t[0], t[1], t[2], t[3]);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      e2m1x8_to_bf16(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w, X, t);
+      const uint4 v = make_uint4(t[0], t[1], t[2], t[3]);
+      if (i == 0) o[0] = v;
+      if (i == 1) o[1] = v;
+      if (i == 2) o[2] = v;
+      if (i == 3) o[3] = v;
+    }
+  }
 }
 
 // Nearest E2M1 code of a (already scaled) value, ties to the even code, saturating.

@@ -84,6 +84,21 @@ __device__ __forceinline__ long long kv_row(const KvCache& k, int req, long long
   }
   return r < k.n_rows ? r : -1;
 }
+// The same for an entry given in 32 bits (0 <= e), without 64-bit divisions.
+__device__ __forceinline__ long long kv_row32(const KvCache& k, int req, int e) {
+  long long r;
+  if (k.bt) {
+    const unsigned int j = (unsigned int)e / (unsigned int)k.rpb;
+    if (j >= k.bt_stride) return -1;
+    const int blk = k.bt[req * k.bt_stride + j];
+    if (blk < 0) return -1;
+    r = (long long)blk * k.rpb + (int)(e - j * k.rpb);
+  } else {
+    if (e >= k.seq_rows) return -1;
+    r = req * k.seq_rows + e;
+  }
+  return r < k.n_rows ? r : -1;
+}
 struct KvAppend {
   const void* x;
   bool x_f32;

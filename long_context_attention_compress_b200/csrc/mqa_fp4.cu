@@ -5,6 +5,10 @@
 // An entry's row is code * 2^X per 32 channels on its first c - rope_dims channels and bf16 on the rest; both are
 // exact in bf16.
 
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "common.cuh"
 #include "formats.cuh"
 #include "internal.h"
@@ -49,7 +53,7 @@ __device__ __forceinline__ const bf16* window_row(const MqaFp4Problem& p, const 
   return p.win + r.req * p.win_seq_stride + (long long)((r.tok0 + w) % p.win_rows) * p.kv.c;
 }
 
-// ---- CUDA cores: any c up to 512 ------------------------------------------------------
+// ---- CUDA cores: c other than 512 ------------------------------------------------------
 // One CTA per (query, group of kSH heads, split): rows are widened into shared memory 16 at a time, an online softmax
 // runs over them, and the state (m, l, o) goes to the combine kernel.
 constexpr int kSThreads = 256, kSRows = 16, kSH = 4;
@@ -156,11 +160,536 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
   }
   if (tid < nh) ws_ml[st * p.H + h0 + tid] = make_float2(s_m[tid], s_l[tid]);
 }
+
+// ---- tcgen05: c = 512 -------------------------------------------------------------------
+// Rows are the MMA's M dimension and heads its N dimension (64 heads a CTA; fewer are padded with zero queries):
+// a 128-row tile, widened to bf16 in shared memory (128B-swizzled, eight 64-channel chunks), is the K-major A operand
+// of S^T = R . Q^T and, read MN-major, the A operand of O^T += V^T . P^T.  It is tracked as four 128-channel blocks:
+// PV releases them one by one, the converters refill them with the next tile, and QK^T of that tile follows block by
+// block.  The last chunk has two buffers that tiles use in turn, so that the usual 64 rotary channels are copied a
+// tile ahead.
+//   warp 0        MMA issuer (and TMEM owner); warps 1-3 only complete its warpgroup
+//   warps 4-11    softmax: two per TMEM lane quarter (32 rows), 32 heads each; P = 2^(s - m) rounded to bf16, the
+//                 row sums in f32 from the rounded values, formed after P has been handed over; accumulators
+//                 rescaled only when some head's maximum grows by more than 2^8
+//   warps 12-27   converters: eight rows a warp, thread = (row, one of a block's four 32-channel groups), so that a
+//                 warp's load touches eight rows' lines, not 32; the next tile's codes are loaded, and three of its
+//                 blocks widened into registers, while QK^T and the softmax run, so that only stores lie between
+//                 PV releasing a block and the next QK^T over it; rotary channels and window rows are copied with
+//                 16-byte cp.async
+constexpr int kSoft = 8, kConv = 16;
+constexpr int kThreads = 32 * (4 + kSoft + kConv);   // whole warpgroups, for the register split
+constexpr int kRowsT = 128;                          // rows per tile
+constexpr int kC = 512, kHT = 64;                    // channels; heads per CTA
+constexpr int kBlocks = 4;                           // 128-channel blocks of a tile
+constexpr uint32_t kQChunk = kHT * 128;              // 8 KiB: 64 channels of the queries
+constexpr uint32_t kKvChunk = kRowsT * 128;          // 16 KiB: 64 channels of the tile
+constexpr uint32_t kQBytes = 8 * kQChunk, kKvBytes = 8 * kKvChunk, kPBytes = kRowsT * kHT * 2;
+constexpr uint32_t kOffQ = 0, kOffKv = kQBytes, kOffP = kOffKv + kKvBytes, kOffR2 = kOffP + kPBytes;
+constexpr uint32_t kOffBars = kOffR2 + kKvChunk;
+constexpr uint32_t kR2Delta = kOffR2 - (kOffKv + 7 * kKvChunk);  // second buffer of the last chunk, after the first
+constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kHpt = kHT * 4 / kSoft;                // heads per softmax thread (32)
+constexpr int kOutLd = kC + 8;                       // staged output row (bf16), padded against bank conflicts
+
+struct __align__(16) Bars {
+  float red[4][kHT];
+  float mref[kHT];
+  float alpha[kHT];
+  uint64_t qfull, vfull[kBlocks], vempty[kBlocks], sfull, pfull, odone, drain;
+  uint32_t rowok[4][kConv];  // [tile % 4][converter warp]: bit 4 j is set where row j of the warp's eight takes part
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmemBytes = 1024 + kOffBars + sizeof(Bars);
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kHT * kOutLd * 2 <= kKvBytes, "staged output fits in the tile buffer");
+
+// One reduce-scatter step over lane bit O: of the NV values held, keep the half selected by the bit and fold in the
+// partner's copy of that half.
+template <int O, int NV, bool MAX>
+__device__ __forceinline__ void rs_step(float (&a)[kHpt], int lane) {
+  const bool hi = (lane & O) != 0;
+#pragma unroll
+  for (int j = 0; j < NV / 2; ++j) {
+    const float send = hi ? a[j] : a[j + NV / 2];
+    const float keep = hi ? a[j + NV / 2] : a[j];
+    const float got = __shfl_xor_sync(0xffffffffu, send, O);
+    a[j] = MAX ? fmaxf(keep, got) : keep + got;
+  }
+}
+// Afterwards lane l holds the warp-wide maximum (or sum) of value l.
+template <bool MAX>
+__device__ __forceinline__ float warp_reduce32(float (&a)[kHpt], int lane) {
+  rs_step<16, 32, MAX>(a, lane);
+  rs_step<8, 16, MAX>(a, lane);
+  rs_step<4, 8, MAX>(a, lane);
+  rs_step<2, 4, MAX>(a, lane);
+  rs_step<1, 2, MAX>(a, lane);
+  return a[0];
+}
+
+// The tiles of list positions [ub, ue): entries, then window rows, each cut from its own start.
+struct Tiles {
+  int a0, a1, w0, w1, na, n;
+  __device__ __forceinline__ Tiles(int entries, int window, int ub, int ue) {
+    a0 = min(ub, entries);
+    a1 = min(ue, entries);
+    w0 = min(max(ub - entries, 0), window);
+    w1 = min(max(ue - entries, 0), window);
+    na = (a1 - a0 + kRowsT - 1) / kRowsT;
+    n = na + (w1 - w0 + kRowsT - 1) / kRowsT;
+  }
+  __device__ __forceinline__ int first(int i) const { return i < na ? a0 + i * kRowsT : w0 + (i - na) * kRowsT; }
+  __device__ __forceinline__ int rows(int i) const { return min(kRowsT, (i < na ? a1 : w1) - first(i)); }
+};
+
+__global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                                                                 MqaFp4Problem p, int splits, int rows_per_split,
+                                                                 float* __restrict__ ws_o,
+                                                                 float2* __restrict__ ws_ml) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base = tc::smem_align1024(smem_raw);
+  Bars* bars = reinterpret_cast<Bars*>(base + kOffBars);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = (p.H + kHT - 1) / kHT;
+  const int sp = blockIdx.x % splits;
+  const int hg = (blockIdx.x / splits) % groups;
+  const int q = blockIdx.x / splits / groups;
+  const int h0 = hg * kHT;
+
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->qfull, 1);
+    for (int b = 0; b < kBlocks; ++b) {
+      tc::mbar_init(&bars->vfull[b], kConv);
+      tc::mbar_init(&bars->vempty[b], 1);
+    }
+    tc::mbar_init(&bars->sfull, 1);
+    tc::mbar_init(&bars->pfull, kSoft);
+    tc::mbar_init(&bars->odone, 1);
+    tc::mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    tc::fence_mbar_init();
+  }
+  for (int h = threadIdx.x; h < kHT; h += kThreads) bars->mref[h] = neg_inf();
+  if (warp == 0) tc::tmem_alloc(&bars->tmem_base, kTmemCols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars->tmem_base;
+  tc::griddep_launch_dependents();
+
+  const Rows r = rows_of(p, q);
+  const int ub = sp * rows_per_split;
+  const Tiles tiles(r.entries, r.window, ub, ub + rows_per_split);
+  const int nt = tiles.n;
+
+  if (warp < 4) {
+    // ------------------------------ MMA issuer ------------------------------
+    tc::setmaxnreg_dec<24>();
+    if (warp == 0 && nt > 0) {
+      const bool lead = tc::elect_one();
+      if (lead) {
+        tc::mbar_arrive_expect_tx(&bars->qfull, kQBytes);
+        for (int ch = 0; ch < 8; ++ch) tc::tma_load_3d(base + kOffQ + ch * kQChunk, &tm_q, &bars->qfull, ch * 64, h0, q);
+      }
+      __syncwarp();
+      constexpr uint32_t id_qk = tc::idesc_bf16_f32(kRowsT, kHT, false, false);
+      constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, kHT, true, true);
+      const uint64_t q_desc0 = tc::sdesc_sw128(tc::smem_u32(base + kOffQ), 16, 1024);
+      const uint64_t k_desc0 = tc::sdesc_sw128(tc::smem_u32(base + kOffKv), 16, 1024);
+      const uint64_t v_desc0 = tc::sdesc_sw128(tc::smem_u32(base + kOffKv), kKvChunk, 1024);
+      // the last block with the second buffer of the last chunk
+      const uint64_t v_desc3 = tc::sdesc_sw128(tc::smem_u32(base + kOffKv + 6 * kKvChunk), kKvChunk + kR2Delta, 1024);
+      const uint64_t p_desc0 = tc::sdesc_sw128(tc::smem_u32(base + kOffP), kPBytes, 1024);
+      bool ok = tc::warp_wait(&bars->qfull, 0, abort);
+      for (int i = 0; ok && i < nt; ++i) {
+        const uint32_t ph = i & 1;
+        // S(i-1) has been read: P(i-1), which PV(i-1) waited for, was written after
+#pragma unroll 1
+        for (int b = 0; b < kBlocks; ++b) {
+          if (!(ok = tc::warp_wait(&bars->vfull[b], ph, abort))) break;
+          tc::fence_after_sync();
+          const uint64_t kd = k_desc0 + b * (2 * kKvChunk >> 4), qd = q_desc0 + b * (2 * kQChunk >> 4);
+          const uint64_t kd2 = kd + ((kKvChunk + (b == kBlocks - 1 && ph ? kR2Delta : 0u)) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_lead(lead, tmem + kColS, kd + 2 * k, qd + 2 * k, id_qk, b + k > 0 ? 1u : 0u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_lead(lead, tmem + kColS, kd2 + 2 * k, qd + (kQChunk >> 4) + 2 * k, id_qk, 1u);
+        }
+        if (!ok) break;
+        if (lead) tc::mma_commit(&bars->sfull);
+        __syncwarp();
+        if (!(ok = tc::warp_wait(&bars->pfull, ph, abort))) break;
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int b = 0; b < kBlocks; ++b) {
+          const uint64_t vd = b == kBlocks - 1 && ph ? v_desc3 : v_desc0 + b * (2 * kKvChunk >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kRowsT / 16; ++kk)
+            tc::mma_bf16_lead(lead, tmem + kColO + b * kHT, vd + kk * (2048 >> 4), p_desc0 + kk * (2048 >> 4), id_pv,
+                              i + kk > 0 ? 1u : 0u);
+          if (lead) tc::mma_commit(&bars->vempty[b]);  // the converters may refill this block
+          __syncwarp();
+        }
+        if (lead) tc::mma_commit(&bars->odone);
+        __syncwarp();
+      }
+      if (lead) {
+        tc::mma_commit(&bars->drain);
+        for (uint32_t k = 0; k < tc::kSpinLimit && !tc::mbar_try_wait(&bars->drain, 0); ++k) __nanosleep(64);
+        for (uint32_t k = 0; k < tc::kSpinLimit && !tc::mbar_try_wait(&bars->qfull, 0); ++k) __nanosleep(64);
+      }
+    }
+  } else if (warp < 4 + kSoft) {
+    tc::setmaxnreg_dec<64>();
+
+    // ------------------------------ softmax ------------------------------
+    const int quarter = warp & 3, hsel = (warp - 4) >> 2;  // TMEM lanes of this warp; heads [32 hsel, 32 hsel + 32)
+    const int row = quarter * 32 + lane, st = threadIdx.x - 128;
+    const uint32_t lanebase = (uint32_t)(quarter * 32) << 16;
+    const float scale_log2 = p.scale * kLog2e;
+    float lw = 0.f;  // lane l: head 32 hsel + l's sum over this warp's rows, relative to the running maximum
+    bool failed = false;
+    for (int i = 0; i < nt; ++i) {
+      const uint32_t ph = i & 1;
+      float sv[kHpt];
+      bool need = false;  // some score lies above its head's running maximum + 2^8 (or is the first one)
+      // (block 0 landed long before S: this wait orders the converters' row flags before their use here)
+      failed = !tc::warp_wait(&bars->vfull[0], ph, abort) || !tc::warp_wait(&bars->sfull, ph, abort);
+      const bool valid = !failed && ((bars->rowok[i & 3][row >> 3] >> (4 * (row & 7))) & 1u);
+      auto load_scores = [&]() {
+        uint32_t v[kHpt];
+        tc::tmem_ld32(tmem + lanebase + kColS + kHpt * hsel, v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < kHpt; ++h) sv[h] = valid ? __uint_as_float(v[h]) * scale_log2 : neg_inf();
+      };
+      if (!failed) tc::fence_after_sync();
+      load_scores();
+#pragma unroll
+      for (int c = 0; c < kHpt / 4; ++c) {
+        const float4 m4 = *reinterpret_cast<const float4*>(bars->mref + kHpt * hsel + 4 * c);
+        need |= sv[4 * c] > m4.x + kRescaleLog2;
+        need |= sv[4 * c + 1] > m4.y + kRescaleLog2;
+        need |= sv[4 * c + 2] > m4.z + kRescaleLog2;
+        need |= sv[4 * c + 3] > m4.w + kRescaleLog2;
+      }
+      // one vote for "nobody needs new maxima and nobody failed", the usual case
+      if (tc::named_bar_or(1, 32 * kSoft, need || failed || *abort)) {
+        if (tc::named_bar_or(1, 32 * kSoft, failed || *abort)) { failed = true; break; }
+        bars->red[quarter][kHpt * hsel + lane] = warp_reduce32<true>(sv, lane);  // (the scores are read again below)
+        tc::named_bar(1, 32 * kSoft);
+        if (st < kHT) {
+          const float mt = fmaxf(fmaxf(bars->red[0][st], bars->red[1][st]), fmaxf(bars->red[2][st], bars->red[3][st]));
+          const float mo = bars->mref[st];
+          const bool grow = mt > mo + kRescaleLog2;  // -inf + 2^8 = -inf: any first score
+          bars->alpha[st] = grow ? (mo == neg_inf() ? 0.f : fast_exp2(mo - mt)) : 1.f;
+          if (grow) bars->mref[st] = mt;
+        }
+        tc::named_bar(1, 32 * kSoft);
+        lw *= bars->alpha[kHpt * hsel + lane];
+        if (i > 0) {
+          // O^T holds the sums up to tile i-1 (PV(i-1) was issued before QK(i), whose commit has arrived)
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int b = 0; b < kBlocks; ++b) {
+            const uint32_t ta = tmem + lanebase + kColO + b * kHT + kHpt * hsel;
+            uint32_t v[kHpt];
+            tc::tmem_ld32(ta, v);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < kHpt; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * bars->alpha[kHpt * hsel + h]);
+            tc::tmem_st32(ta, v);
+          }
+          tc::tmem_st_wait();
+        }
+        load_scores();
+      }
+      tc::fence_before_sync();
+      // P(i): PV(i-1), the last reader of the buffer, has completed
+      unsigned char* prow = base + kOffP + row * 128;
+#pragma unroll
+      for (int cc = 0; cc < kHpt / 8; ++cc) {
+        const int c = (kHpt / 8) * hsel + cc;  // 16-byte unit of the row: heads 8c .. 8c+7
+        const float4 ma = *reinterpret_cast<const float4*>(bars->mref + c * 8);
+        const float4 mb = *reinterpret_cast<const float4*>(bars->mref + c * 8 + 4);
+        const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int h = cc * 8 + 2 * j;
+          const float m0 = mm[2 * j], m1 = mm[2 * j + 1];
+          const float p0 = (m0 == neg_inf()) ? 0.f : fast_exp2(sv[h] - m0);
+          const float p1 = (m1 == neg_inf()) ? 0.f : fast_exp2(sv[h + 1] - m1);
+          w[j] = pack_bf16x2(p0, p1);
+          sv[h] = bf16_lo(w[j]);  // exactly what PV multiplies
+          sv[h + 1] = bf16_hi(w[j]);
+        }
+        *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->pfull);
+      lw += warp_reduce32<false>(sv, lane);
+    }
+    // ---- epilogue: O^T (channels x heads) and l ----
+    bars->red[quarter][kHpt * hsel + lane] = lw;
+    bool ok = !failed;
+    if (ok && nt > 0) ok = tc::warp_wait(&bars->odone, (nt - 1) & 1, abort);
+    ok = !tc::named_bar_or(1, 32 * kSoft, !ok || *abort);
+    if (ok) {
+      tc::fence_after_sync();
+      const int dl = quarter * 32 + lane;  // channel within its block
+      float lv[kHpt];
+#pragma unroll
+      for (int h = 0; h < kHpt; ++h) {
+        const int hh = kHpt * hsel + h;
+        lv[h] = (bars->red[0][hh] + bars->red[1][hh]) + (bars->red[2][hh] + bars->red[3][hh]);
+      }
+      if (splits == 1) {
+#pragma unroll
+        for (int h = 0; h < kHpt; ++h) {
+          const int hh = kHpt * hsel + h;
+          // a sink logit joins the denominator here (base-2, against the head's running maximum)
+          if (p.sink != nullptr && h0 + hh < p.H && lv[h] > 0.f)
+            lv[h] += fast_exp2(p.sink[h0 + hh] * kLog2e - bars->mref[hh]);
+          lv[h] = lv[h] > 0.f ? __fdividef(1.f, lv[h]) : 0.f;
+        }
+        const int rope0 = kC - p.rope_dims;
+        bf16* stage = reinterpret_cast<bf16*>(base + kOffKv);  // the last PV has read the tile
+#pragma unroll 1
+        for (int b = 0; b < kBlocks; ++b) {
+          uint32_t v[kHpt];
+          if (nt > 0) {
+            tc::tmem_ld32(tmem + lanebase + kColO + b * kHT + kHpt * hsel, v);
+            tc::tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int h = 0; h < kHpt; ++h) v[h] = 0u;
+          }
+          const int d = b * 128 + dl;
+          // output rotation by -t: channel d pairs with d ^ 1, the neighbouring lane; whole warps take the branch
+          const bool rot = p.rope_dims > 0 && b * 128 + quarter * 32 + 31 >= rope0;
+          float rc = 1.f, rs = 0.f;
+          if (rot && d >= rope0) {
+            float sn;
+            rope_cos_sin(r.t, (d - rope0) >> 1, p.rope_dims, p.rope_base, rc, sn);
+            rs = (d & 1) ? -sn : sn;
+          }
+#pragma unroll
+          for (int h = 0; h < kHpt; ++h) {
+            float o = lv[h] != 0.f ? __uint_as_float(v[h]) * lv[h] : 0.f;
+            if (rot) o = fmaf(o, rc, __shfl_xor_sync(0xffffffffu, o, 1) * rs);
+            stage[(kHpt * hsel + h) * kOutLd + d] = __float2bfloat16_rn(o);
+          }
+        }
+        tc::named_bar(1, 32 * kSoft);
+        bf16* out = p.out + ((long long)q * p.H + h0) * kC;
+        const int nh = min(kHT, p.H - h0);
+        for (int u = st; u < nh * (kC / 8); u += 32 * kSoft) {
+          const int h = u / (kC / 8), x = u % (kC / 8);
+          *reinterpret_cast<uint4*>(out + h * kC + x * 8) = *reinterpret_cast<const uint4*>(stage + h * kOutLd + x * 8);
+        }
+      } else {
+        const long long part = ((long long)q * splits + sp) * p.H + h0;
+        float* wo = ws_o + part * kC;
+#pragma unroll 1
+        for (int b = 0; b < kBlocks; ++b) {
+          uint32_t v[kHpt];
+          if (nt > 0) {
+            tc::tmem_ld32(tmem + lanebase + kColO + b * kHT + kHpt * hsel, v);
+            tc::tmem_ld_wait();
+          }
+#pragma unroll
+          for (int h = 0; h < kHpt; ++h) {
+            const int hh = kHpt * hsel + h;
+            if (h0 + hh < p.H) wo[hh * kC + b * 128 + dl] = nt > 0 ? __uint_as_float(v[h]) : 0.f;
+          }
+        }
+        if (st < kHT && h0 + st < p.H) {
+          const float l = (bars->red[0][st] + bars->red[1][st]) + (bars->red[2][st] + bars->red[3][st]);
+          ws_ml[part + st] = make_float2(l > 0.f ? bars->mref[st] : neg_inf(), l);
+        }
+      }
+    }
+  } else {
+    // ------------------------------ converters ------------------------------
+    tc::setmaxnreg_inc<88>();
+    const int cw = warp - 4 - kSoft;
+    const int row = 8 * cw + (lane >> 2), sub = lane & 3;    // row of the tile; group 4b + sub of block b
+    const int n_groups = (kC - p.kv.rope_dims) / kFp4Group;  // groups held in 4 bits
+    const bool rope64 = p.kv.rope_dims == 64;                // the last chunk is copied a tile ahead
+    const uint8_t* codes = reinterpret_cast<const uint8_t*>(p.kv.codes) + sub * 16;
+    const uint8_t* scales = reinterpret_cast<const uint8_t*>(p.kv.scales);
+    const int chunk = sub >> 1;                              // of a block's two
+    const uint32_t sw = row & 7;
+    // This thread's 16-byte units of its chunk's row are unit0 ^ w, w = 0 .. 3: with the swizzle, the eight lanes of a
+    // store phase (two rows, four groups) hit eight different units.
+    const uint32_t unit0 = 4 * (sub & 1) + 2 * chunk;
+    unsigned char* kv = base + kOffKv + row * 128;
+    // Entry of this thread's row of tile i, and its cache row (-1: none).
+    auto entry_of = [&](int i) -> int {
+      if (i >= tiles.na || row >= tiles.rows(i)) return -1;
+      const int u = tiles.first(i) + row;
+      return r.idx ? r.idx[u] : u;
+    };
+    auto resolve = [&](int i, int e) -> int {
+      if (p.check && sub == 0 && r.idx && i < tiles.na && row < tiles.rows(i)) {
+        const unsigned int k = entry_check(e, r.t, p.rate, p.N);
+        if (k) atomicOr(&g_mqa_fp4_error, k << 1);
+      }
+      if (e < 0 || e >= p.N) return -1;
+      const int x = (int)kv_row32(p.kv, r.req, e);
+      if (p.check && x < 0) atomicOr(&g_mqa_fp4_error, kIdxBlock << 1);
+      return x;
+    };
+    // The codes of this thread's group of block b of cache row x, in the order of its stores (halves swapped in the
+    // second chunk).
+    auto fetch = [&](int x, int b) -> uint4 {
+      const uint4 v = x >= 0 && 4 * b + sub < n_groups ? *reinterpret_cast<const uint4*>(codes + x * p.kv.ld_codes + b * 64)
+                                                       : make_uint4(0u, 0u, 0u, 0u);
+      return chunk ? make_uint4(v.z, v.w, v.x, v.y) : v;
+    };
+    auto fetch_scales = [&](int x) -> uint4 {
+      return x >= 0 ? *reinterpret_cast<const uint4*>(scales + x * p.kv.ld_scales) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // This thread's row of chunk c of tile i.
+    auto row_of = [&](int i, int c) -> unsigned char* { return kv + c * kKvChunk + (c == 7 && (i & 1) ? kR2Delta : 0u); };
+    // Copies a quarter of a 128-byte row of chunk c (units 2 sub and 2 sub + 1); zeros where there is none.
+    auto copy_row = [&](int i, int c, const bf16* src, bool ok) {
+      const uint32_t dst = tc::smem_u32(row_of(i, c));
+#pragma unroll
+      for (uint32_t w = 0; w < 2; ++w)
+        tc::cp_async16(dst + (((2 * sub + w) ^ sw) << 4), src + (2 * sub + w) * 8, ok ? 16 : 0);
+    };
+    // The 64 rotary channels of cache row x, into the last chunk of tile i.
+    auto copy_rope = [&](int i, int x) {
+      copy_row(i, 7, p.kv.rope + (x >= 0 ? x * p.kv.ld_rope : 0ll), x >= 0);
+      tc::cp_async_commit();
+    };
+    // Cache rows of the tile being converted and of the next one, the entry of the one after: an index, its block and
+    // its row are dependent loads, each given a tile's time.
+    const int e0 = entry_of(0), e1 = entry_of(1);
+    int x = resolve(0, e0), xn = resolve(1, e1);
+    int e_next = entry_of(2);
+    if (rope64 && tiles.na > 0) copy_rope(0, x);
+    // Widen this thread's group of block b.
+    auto widen = [&](int x, int b, const uint4& v, uint32_t scale_word, uint4 (&o)[4]) {
+      const int g = 4 * b + sub;
+      if (g < n_groups) {
+        e2m1x32_to_bf16(v, (int)((scale_word >> (8 * sub)) & 255u) - 127, o);
+      } else if (!rope64) {
+#pragma unroll
+        for (uint32_t w = 0; w < 4; ++w)
+          o[w] = x >= 0 ? *reinterpret_cast<const uint4*>(p.kv.rope + x * p.kv.ld_rope + (g - n_groups) * 32 +
+                                                          ((2 * chunk) ^ w) * 8)
+                        : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    bool okw = true;
+    // Once block b is free, store a widened group and signal the block.
+    auto put = [&](int i, int b, const uint4 (&o)[4]) {
+      if (!okw || !(okw = tc::warp_wait(&bars->vempty[b], (i & 1) ^ 1, abort))) return;
+      if (4 * b + sub < n_groups || !rope64) {
+        unsigned char* d = row_of(i, 2 * b + chunk);
+#pragma unroll
+        for (uint32_t w = 0; w < 4; ++w) *reinterpret_cast<uint4*>(d + (((unit0 ^ w) ^ sw) << 4)) = o[w];
+      }
+      if (b == kBlocks - 1) tc::cp_async_wait<0>();  // the last chunk, under way since the last tile
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->vfull[b]);
+    };
+    int i = 0;
+    for (; okw && i < tiles.na; ++i) {
+      const uint32_t mask = __ballot_sync(0xffffffffu, x >= 0);
+      if (lane == 0) bars->rowok[i & 3][cw] = mask;
+      uint4 o0[4], o1[4], o2[4];
+      const uint4 sc = fetch_scales(x);
+      const uint4 v0 = fetch(x, 0), v1 = fetch(x, 1), v2 = fetch(x, 2), v3 = fetch(x, 3);
+      const int x2 = resolve(i + 2, e_next);
+      e_next = entry_of(i + 3);
+      widen(x, 0, v0, sc.x, o0);
+      widen(x, 1, v1, sc.y, o1);
+      widen(x, 2, v2, sc.z, o2);
+      put(i, 0, o0);
+      widen(x, 3, v3, sc.w, o0);
+      put(i, 1, o1);
+      put(i, 2, o2);
+      put(i, 3, o0);
+      // PV of tile i-1 has released every block here: its buffer of the last chunk takes tile i+1's
+      if (rope64 && i + 1 < tiles.na) copy_rope(i + 1, xn);
+      x = xn;
+      xn = x2;
+    }
+    for (; okw && i < nt; ++i) {  // window rows
+      const uint32_t ph = i & 1;
+      const bool valid = row < tiles.rows(i);
+      const uint32_t mask = __ballot_sync(0xffffffffu, valid);
+      if (lane == 0) bars->rowok[i & 3][cw] = mask;
+      const bf16* src = valid ? window_row(p, r, tiles.first(i) + row) : p.win;
+#pragma unroll 1
+      for (int b = 0; b < kBlocks; ++b) {
+        if (!tc::warp_wait(&bars->vempty[b], ph ^ 1, abort)) { okw = false; break; }
+        copy_row(i, 2 * b, src + b * 128, valid);
+        copy_row(i, 2 * b + 1, src + b * 128 + 64, valid);
+        tc::cp_async_commit();
+        if (b > 0) {
+          tc::cp_async_wait<1>();
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars->vfull[b - 1]);
+        }
+      }
+      tc::cp_async_wait<0>();
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (okw && lane == 0) tc::mbar_arrive(&bars->vfull[kBlocks - 1]);
+    }
+    tc::cp_async_wait<0>();
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (threadIdx.x == 0 && bars->abort) atomicOr(&g_mqa_fp4_error, 1u);
+  if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
+}
 }  // namespace
 
+extern cudaError_t make_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                                  const uint64_t* strides_bytes, uint32_t box_rows);
+
+// Splits per query: fewest tiles on the critical path over whole waves of CTAs (one per SM), a CTA's set-up and
+// epilogue counted as three quarters of a tile each (tcgen05); about eight CTAs per SM (CUDA cores).
 MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms) {
   MqaPlan pl;
-  pl.max_rows = max(1, (p.idx ? p.n_idx : p.N) + (p.win ? p.n_win : 0));
+  const int entries = p.idx ? p.n_idx : p.N, window = p.win ? p.n_win : 0;
+  pl.max_rows = max(1, entries + window);
+  if (p.kv.c == kC) {
+    const int groups = (p.H + kHT - 1) / kHT;
+    const int tiles = max(1, (entries + kRowsT - 1) / kRowsT + (window + kRowsT - 1) / kRowsT);
+    const long long ctas1 = (long long)max(1, p.Tq) * groups;
+    const int smax = (int)min((long long)min(tiles, 1024), max(1ll, 2ll * num_sms / ctas1));
+    int best = 1;
+    long long best_cost = -1;
+    for (int s = 1; s <= smax; ++s) {
+      const int tpc = (tiles + s - 1) / s, eff = (tiles + tpc - 1) / tpc;
+      const long long waves = (ctas1 * eff + num_sms - 1) / num_sms;
+      const long long cost = waves * (tpc * 4 + 6) + (eff > 1 ? 4 : 0);
+      if (best_cost < 0 || cost < best_cost) { best_cost = cost; best = eff; }
+    }
+    const int tpc = (tiles + best - 1) / best;
+    pl.splits = best;
+    pl.rows_per_split = tpc * kRowsT;
+    pl.ws_bytes = best > 1 ? (size_t)p.Tq * best * p.H * (kC * sizeof(float) + sizeof(float2)) : 0;
+    return pl;
+  }
   const int groups = (p.H + kSH - 1) / kSH;
   int splits = (int)max(1ll, (8ll * num_sms) / max(1ll, (long long)p.Tq * groups));
   splits = min(min(splits, 64), (pl.max_rows + kSRows - 1) / kSRows);
@@ -174,12 +703,27 @@ cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, 
   if (p.Tq == 0) return cudaSuccess;
   float* ws_o = reinterpret_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)p.Tq * pl.splits * p.H * p.kv.c);
-  const int groups = (p.H + kSH - 1) / kSH;
-  mqa_fp4_simple_kernel<<<(unsigned)(p.Tq * groups * pl.splits), kSThreads, 0, stream>>>(p, pl.splits,
-                                                                                        pl.rows_per_split, ws_o, ws_ml);
+  cudaError_t e;
+  if (p.kv.c == kC) {
+    CUtensorMap tm_q;
+    const uint64_t qd[3] = {(uint64_t)kC, (uint64_t)p.H, (uint64_t)p.Tq};
+    const uint64_t qs[2] = {(uint64_t)kC * 2, (uint64_t)p.H * kC * 2};
+    e = make_tmap_bf16(&tm_q, p.q, 3, qd, qs, kHT);  // heads past n_heads read as zeros
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute((const void*)mqa_fp4_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int groups = (p.H + kHT - 1) / kHT;
+    mqa_fp4_tc_kernel<<<(unsigned)(p.Tq * groups * pl.splits), kThreads, kSmemBytes, stream>>>(
+        tm_q, p, pl.splits, pl.rows_per_split, ws_o, ws_ml);
+  } else {
+    const int groups = (p.H + kSH - 1) / kSH;
+    mqa_fp4_simple_kernel<<<(unsigned)(p.Tq * groups * pl.splits), kSThreads, 0, stream>>>(
+        p, pl.splits, pl.rows_per_split, ws_o, ws_ml);
+  }
   ++g_launch_counter;
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  e = cudaGetLastError();
+  if (e != cudaSuccess || (p.kv.c == kC && pl.splits == 1)) return e;
   return launch_mqa_combine(ws_o, ws_ml, p.Tq, pl.splits, p.H, p.kv.c, p.out, p.sink, p.q_pos, p.rope_dims, p.rope_base,
                             stream, true);
 }
