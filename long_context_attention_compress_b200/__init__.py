@@ -24,5 +24,6 @@ _EXPORTS = {
 def __getattr__(name):
     if name in _EXPORTS:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)  # (looked up once)
+        return value
     raise AttributeError(name)

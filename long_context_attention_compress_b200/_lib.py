@@ -165,8 +165,14 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream object (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -350,23 +356,20 @@ HCA_KV_BF16, HCA_KV_FP8, HCA_KV_FP4 = 0, 1, 2
 _FORMS = {"bf16": HCA_KV_BF16, "fp8": HCA_KV_FP8, "fp4": HCA_KV_FP4}
 
 
-def _same_device(device, **tensors):
+def _same_device(*tensors):
     """The kernels run on the current device's stream: every tensor has to live on that device."""
     cur = torch.cuda.current_device()
-    for name, t in dict(tensors, cache=device).items():
-        if t is None:
-            continue
-        d = t if isinstance(t, torch.device) else t.device
-        if d.type != "cuda" or d.index != cur:
-            raise ValueError(f"{name}: on {d}, but the current device is cuda:{cur}")
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, but the current device is cuda:{cur}")
 
 
-def _scratch(need: int, ws, device, stream):
-    """Workspace of `need` bytes: the caller's, or one that lives until the call's work on `stream` is done."""
+def _scratch(need: int, device, stream):
+    """Workspace of `need` bytes that lives until the call's work on `stream` is done."""
     if need == SIZE_MAX:
         raise HcaError(-2, last_error() or "unsupported configuration (workspace query)")
-    if need == 0 or ws is not None:
-        return ws, 0 if ws is None else ws.numel() * ws.element_size()
+    if need == 0:
+        return None, 0
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     if stream is not None:
         ws.record_stream(stream)
@@ -393,7 +396,7 @@ class KvCache:
             want["scales"] = (scales, F32 if form == "fp8" else torch.uint8, n // (64 if form == "fp8" else 32))
             if rope_dims:
                 want["rope"] = (rope, BF16, rope_dims)
-        self.form, self.c, self.rope_dims, self.device = form, c, rope_dims, getattr(codes, "device", None)
+        self.form, self.c, self.rope_dims = form, c, rope_dims
         self.tensors = {k: v[0] for k, v in want.items()}
         d = self.desc = KvCacheDesc()
         d.form, d.c, d.rope_dims, d.ring = _FORMS[form], c, rope_dims, int(bool(ring))
@@ -426,6 +429,8 @@ class KvCache:
             d.block_table, d.rows_per_block = block_table.data_ptr(), codes.shape[1]
         self.tensors["block_table"] = block_table
         self.n_req = d.n_req
+        self.codes = codes  # (the device of all of them)
+        self.ref = ctypes.byref(d)
 
 
 def kv_cache_append(x, cache: KvCache, first, row_start=None, rate=1, gamma=None, rotate=False, norm_eps=1e-6,
@@ -437,7 +442,7 @@ def kv_cache_append(x, cache: KvCache, first, row_start=None, rate=1, gamma=None
         raise TypeError(f"x: dtype {x.dtype}")
     if x.dim() != 2 or x.shape[1] != cache.c or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError(f"x: shape {tuple(x.shape)}, strides {x.stride()}; expected rows of {cache.c} channels")
-    _same_device(cache.device, x=x, first=first, row_start=row_start, gamma=gamma)
+    _same_device(cache.codes, x, first, row_start, gamma)
     B = first.numel()
     if row_start is not None and row_start.numel() != B + 1:
         raise ValueError(f"row_start: {row_start.numel()} values for {B} requests")
@@ -446,22 +451,22 @@ def kv_cache_append(x, cache: KvCache, first, row_start=None, rate=1, gamma=None
     _check(_kv_append(x.data_ptr(), 1 if x.dtype == F32 else 0, x.stride(0) if x.shape[0] > 1 else cache.c, x.shape[0],
                       _ptr(row_start, I32, "row_start"), _ptr(first, I32, "first"), B, int(rate),
                       _ptr(gamma, F32, "gamma"), float(norm_eps), 1 if rotate else 0, float(rope_base),
-                      ctypes.byref(cache.desc), _stream(stream)))
+                      cache.ref, _stream(stream)))
 
 
 def kv_cache_gather(cache: KvCache, B, n_out, idx=None, first=None, out=None, stream=None):
     """Rows of a cache as bf16 [B, n_out, c]: request b's entries idx[b] ([B, n_out] int32; negative: a zero row), or
     first[b] + j ([B] int32), or j."""
-    _same_device(cache.device, idx=idx, first=first, out=out)
+    _same_device(cache.codes, idx, first, out)
     if idx is not None and tuple(idx.shape) != (B, n_out):
         raise ValueError(f"idx: shape {tuple(idx.shape)}, expected {(B, n_out)}")
     if first is not None and first.numel() != B:
         raise ValueError(f"first: {first.numel()} values for {B} requests")
     if out is None:
-        out = torch.empty((B, n_out, cache.c), dtype=BF16, device=cache.device)
+        out = torch.empty((B, n_out, cache.c), dtype=BF16, device=cache.codes.device)
     elif tuple(out.shape) != (B, n_out, cache.c):
         raise ValueError(f"out: shape {tuple(out.shape)}, expected {(B, n_out, cache.c)}")
-    _check(_kv_gather(ctypes.byref(cache.desc), int(B), int(n_out), _ptr(idx, I32, "idx"), _ptr(first, I32, "first"),
+    _check(_kv_gather(cache.ref, int(B), int(n_out), _ptr(idx, I32, "idx"), _ptr(first, I32, "first"),
                       _ptr(out, BF16, "out"), cache.c, n_out * cache.c, _stream(stream)))
     return out
 
@@ -477,7 +482,7 @@ def sparse_mqa_attend_fp4(q, cache: KvCache, N, q_pos, cfg: LayerCfg, idx=None, 
     the request of each query (None: query i belongs to request i).  Other arguments as in sparse_mqa_attend."""
     if q.dim() != 3 or tuple(q.shape[1:]) != (cfg.n_heads, cfg.c):
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [Tq, {cfg.n_heads}, {cfg.c}]")
-    _same_device(cache.device, q=q, q_pos=q_pos, idx=idx, win=win, q_req=q_req, sink=sink, out=out, ws=ws)
+    _same_device(cache.codes, q, q_pos, idx, win, q_req, sink, out, ws)
     Tq = q.shape[0]
     for name, t in (("q_pos", q_pos), ("q_req", q_req)):
         if t is not None and t.numel() != Tq:
@@ -495,8 +500,11 @@ def sparse_mqa_attend_fp4(q, cache: KvCache, N, q_pos, cfg: LayerCfg, idx=None, 
     n_idx = 0 if idx is None else idx.shape[1]
     if rate is None:
         rate = cfg.m if idx is not None else cfg.m_hca
-    ws, nb = _scratch(sparse_mqa_attend_fp4_workspace(cfg, Tq, N, n_idx), ws, q.device, stream)
-    _check(_mqa_fp4(_ptr(q, BF16, "q"), ctypes.byref(cache.desc), int(N), _ptr(idx, I32, "idx"), n_idx, int(rate),
+    if ws is None:
+        ws, nb = _scratch(sparse_mqa_attend_fp4_workspace(cfg, Tq, N, n_idx), q.device, stream)
+    else:
+        nb = ws.numel() * ws.element_size()
+    _check(_mqa_fp4(_ptr(q, BF16, "q"), cache.ref, int(N), _ptr(idx, I32, "idx"), n_idx, int(rate),
                     _ptr(win, BF16, "win"), 0 if win is None else win.shape[1] * win.shape[2],
                     0 if win is None else win.shape[1], _ptr(q_pos, I32, "q_pos"), _ptr(q_req, I32, "q_req"), Tq,
                     ctypes.byref(cfg), _ptr(sink, F32, "sink"), 1 if rotate_out else 0, _ptr(out, BF16, "out"),

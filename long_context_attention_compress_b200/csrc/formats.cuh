@@ -2,6 +2,7 @@
 // power-of-two scale per 32 channels) and FP8 (E4M3 elements, one f32 scale per 64 channels).
 #pragma once
 
+#include <cuda_fp16.h>
 #include <string.h>
 
 #include "common.cuh"
@@ -30,34 +31,31 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
 // and a mask line them up with the high bytes of those elements.  2^X is applied by one
 // bf16x2 multiply, exact while every nonzero product stays a normal bf16
 // (|X| <= 125: 0.5 * 2^X .. 6 * 2^X); beyond that the values are formed in f32 (as
-// exact) and rounded once.  (_normal: for |X| <= 125.)
-__device__ __forceinline__ void e2m1x8_to_bf16_normal(uint32_t w, int X, uint32_t* o) {
-  constexpr uint32_t kHiLo = 0x3F3F3F00u, kHiHi = 0x40404040u, kLoLo = 0xC0800000u, kLoHi = 0xC0804000u;
-  const uint32_t w4 = w << 4, wh = w >> 16;
-  // high bytes of elements 0-3 and 4-7, signs included; low bytes likewise
-  const uint32_t h0 = __byte_perm(kHiLo, kHiHi, w) | (__byte_perm(w4, w, 0x5140u) & 0x80808080u);
-  const uint32_t h1 = __byte_perm(kHiLo, kHiHi, wh) | (__byte_perm(w4, w, 0x7362u) & 0x80808080u);
-  const uint32_t l0 = __byte_perm(kLoLo, kLoHi, w), l1 = __byte_perm(kLoLo, kLoHi, wh);
-  uint32_t p[4];
-  p[0] = __byte_perm(l0, h0, 0x5140u);
-  p[1] = __byte_perm(l0, h0, 0x7362u);
-  p[2] = __byte_perm(l1, h1, 0x5140u);
-  p[3] = __byte_perm(l1, h1, 0x7362u);
-  const uint32_t sb = (uint32_t)(127 + X) << 7;  // bf16 bits of 2^X
-  const uint32_t sbits = sb | (sb << 16);
-  __nv_bfloat162 sc;
-  memcpy(&sc, &sbits, 4);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    __nv_bfloat162 v;
-    memcpy(&v, &p[k], 4);
-    v = __hmul2(v, sc);
-    memcpy(&o[k], &v, 4);
-  }
-}
+// exact) and rounded once.
 __device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, int X, uint32_t* o) {
+  constexpr uint32_t kHiLo = 0x3F3F3F00u, kHiHi = 0x40404040u, kLoLo = 0xC0800000u, kLoHi = 0xC0804000u;
   if (X >= -125 && X <= 125) {
-    e2m1x8_to_bf16_normal(w, X, o);
+    const uint32_t w4 = w << 4, wh = w >> 16;
+    // high bytes of elements 0-3 and 4-7, signs included; low bytes likewise
+    const uint32_t h0 = __byte_perm(kHiLo, kHiHi, w) | (__byte_perm(w4, w, 0x5140u) & 0x80808080u);
+    const uint32_t h1 = __byte_perm(kHiLo, kHiHi, wh) | (__byte_perm(w4, w, 0x7362u) & 0x80808080u);
+    const uint32_t l0 = __byte_perm(kLoLo, kLoHi, w), l1 = __byte_perm(kLoLo, kLoHi, wh);
+    uint32_t p[4];
+    p[0] = __byte_perm(l0, h0, 0x5140u);
+    p[1] = __byte_perm(l0, h0, 0x7362u);
+    p[2] = __byte_perm(l1, h1, 0x5140u);
+    p[3] = __byte_perm(l1, h1, 0x7362u);
+    const uint32_t sb = (uint32_t)(127 + X) << 7;  // bf16 bits of 2^X
+    const uint32_t sbits = sb | (sb << 16);
+    __nv_bfloat162 sc;
+    memcpy(&sc, &sbits, 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      __nv_bfloat162 v;
+      memcpy(&v, &p[k], 4);
+      v = __hmul2(v, sc);
+      memcpy(&o[k], &v, 4);
+    }
     return;
   }
   const float scf = ldexpf(1.f, X);
@@ -66,27 +64,56 @@ __device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, int X, uint32_t* o) {
     o[j >> 1] = pack_bf16x2(e2m1_value((w >> (4 * j)) & 15u) * scf, e2m1_value((w >> (4 * j + 4)) & 15u) * scf);
 }
 
-// A whole MXFP4 block: 32 codes (16 bytes) times 2^X -> 32 bf16 as four 16-byte words; one branch for all of it, so
-// that the four words' instructions interleave.
+// Byte permute whose selector nibbles are below 8 (what __byte_perm would first mask them to).
+__device__ __forceinline__ uint32_t prmt_raw(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+// A whole MXFP4 block: 32 codes (16 bytes) times 2^X -> 32 bf16 as four 16-byte words, for scale bytes below 255.
+// Straight-line code for every X: both multiplications are exact, or round to the bf16 subnormal or infinity that the
+// value has (2^-127 itself is a subnormal factor, which both take).  The byte-table form above is bound by the ALU
+// pipe (14 half-rate instructions per 8 codes), so two of the four words go through the conversion instruction
+// instead (E2M1 -> f16 -> f32, times 2^X, -> bf16), whose middle steps run on the FMA pipe.
 __device__ __forceinline__ void e2m1x32_to_bf16(const uint4& w, int X, uint4* o) {
+  const uint32_t e = (uint32_t)(127 + X);
+  const float scf = __uint_as_float(e ? e << 23 : 0x00400000u);
+  const uint32_t sb = e ? e << 7 : 0x0040u, sbits = sb | (sb << 16);  // 2^X twice, as bf16
   const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-  uint32_t t[4];
-  if (X >= -125 && X <= 125) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e2m1x8_to_bf16_normal(c[i], X, t);
-      o[i] = make_uint4(t[0], t[1], t[2], t[3]);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t t[4];
+    if (i & 1) {
+      constexpr uint32_t kHiLo = 0x3F3F3F00u, kHiHi = 0x40404040u, kLoLo = 0xC0800000u, kLoHi = 0xC0804000u;
+      const uint32_t x = c[i], x4 = x << 4, m = x & 0x77777777u, mh = m >> 16;
+      const uint32_t h0 = prmt_raw(kHiLo, kHiHi, m) | (prmt_raw(x4, x, 0x5140u) & 0x80808080u);
+      const uint32_t h1 = prmt_raw(kHiLo, kHiHi, mh) | (prmt_raw(x4, x, 0x7362u) & 0x80808080u);
+      const uint32_t l0 = prmt_raw(kLoLo, kLoHi, m), l1 = prmt_raw(kLoLo, kLoHi, mh);
+      t[0] = prmt_raw(l0, h0, 0x5140u);
+      t[1] = prmt_raw(l0, h0, 0x7362u);
+      t[2] = prmt_raw(l1, h1, 0x5140u);
+      t[3] = prmt_raw(l1, h1, 0x7362u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t[k]) : "r"(t[k]), "r"(sbits));
+    } else {
+      uint32_t h[4];
+      asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+          "mov.b32 {a, b, c, d}, %4;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+          : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+          : "r"(c[i]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        __half2 v;
+        memcpy(&v, &h[k], 4);
+        const float2 f = __half22float2(v);
+        t[k] = pack_bf16x2(f.x * scf, f.y * scf);
+      }
     }
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      e2m1x8_to_bf16(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w, X, t);
-      const uint4 v = make_uint4(t[0], t[1], t[2], t[3]);
-      if (i == 0) o[0] = v;
-      if (i == 1) o[1] = v;
-      if (i == 2) o[2] = v;
-      if (i == 3) o[3] = v;
-    }
+    o[i] = make_uint4(t[0], t[1], t[2], t[3]);
   }
 }
 

@@ -84,20 +84,21 @@ __device__ __forceinline__ long long kv_row(const KvCache& k, int req, long long
   }
   return r < k.n_rows ? r : -1;
 }
-// The same for an entry given in 32 bits (0 <= e), without 64-bit divisions.
-__device__ __forceinline__ long long kv_row32(const KvCache& k, int req, int e) {
-  long long r;
-  if (k.bt) {
-    const unsigned int j = (unsigned int)e / (unsigned int)k.rpb;
-    if (j >= k.bt_stride) return -1;
-    const int blk = k.bt[req * k.bt_stride + j];
-    if (blk < 0) return -1;
-    r = (long long)blk * k.rpb + (int)(e - j * k.rpb);
-  } else {
-    if (e >= k.seq_rows) return -1;
-    r = req * k.seq_rows + e;
-  }
-  return r < k.n_rows ? r : -1;
+// Division of 0 <= x < 2^31 by a fixed d >= 1 without a divide instruction sequence: q = floor(m x / 2^(31 + s)) with
+// m = ceil(2^(31 + s) / d), 2^(s-1) < d <= 2^s (exact for such x, since m d - 2^(31+s) < d <= 2^s).
+struct FastDiv {
+  uint32_t m, s, d;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  f.d = d;
+  f.s = 0;
+  while ((1ull << f.s) < d) ++f.s;
+  f.m = (uint32_t)(((1ull << (31 + f.s)) + d - 1) / d);
+  return f;
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t x, const FastDiv& f) {
+  return (uint32_t)(((uint64_t)x * f.m) >> 31 >> f.s);
 }
 struct KvAppend {
   const void* x;
@@ -324,6 +325,7 @@ struct MqaFp4Problem {
   const int32_t* q_pos;
   const int32_t* q_req;     // [Tq] or nullptr: query i belongs to request i
   int Tq, H;
+  FastDiv rpb;              // (set by launch_mqa_fp4)
   float scale;
   const float* sink;
   int rope_dims;            // > 0: the output's last rope_dims channels turn back by -q_pos

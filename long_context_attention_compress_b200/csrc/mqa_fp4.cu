@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
 //                 row sums in f32 from the rounded values, formed after P has been handed over; accumulators
 //                 rescaled only when some head's maximum grows by more than 2^8
 //   warps 12-27   converters: eight rows a warp, thread = (row, one of a block's four 32-channel groups), so that a
-//                 warp's load touches eight rows' lines, not 32; the next tile's codes are loaded, and three of its
-//                 blocks widened into registers, while QK^T and the softmax run, so that only stores lie between
-//                 PV releasing a block and the next QK^T over it; rotary channels and window rows are copied with
+//                 warp's load touches eight rows' lines, not 32; the next tile's codes are loaded and widened into
+//                 registers while QK^T and the softmax run, so that only stores lie between PV releasing a block
+//                 and the next QK^T over it; rotary channels and window rows are copied with
 //                 16-byte cp.async
 constexpr int kSoft = 8, kConv = 16;
 constexpr int kThreads = 32 * (4 + kSoft + kConv);   // whole warpgroups, for the register split
@@ -190,6 +190,7 @@ constexpr uint32_t kOffBars = kOffR2 + kKvChunk;
 constexpr uint32_t kR2Delta = kOffR2 - (kOffKv + 7 * kKvChunk);  // second buffer of the last chunk, after the first
 constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
+constexpr float kNoMax = -1e30f;                      // running maximum of a head without a score yet (finite: -inf - kNoMax = -inf)
 constexpr int kHpt = kHT * 4 / kSoft;                // heads per softmax thread (32)
 constexpr int kOutLd = kC + 8;                       // staged output row (bf16), padded against bank conflicts
 
@@ -209,7 +210,7 @@ static_assert(kHT * kOutLd * 2 <= kKvBytes, "staged output fits in the tile buff
 // One reduce-scatter step over lane bit O: of the NV values held, keep the half selected by the bit and fold in the
 // partner's copy of that half.
 template <int O, int NV, bool MAX>
-__device__ __forceinline__ void rs_step(float (&a)[kHpt], int lane) {
+__device__ __forceinline__ void rs_step(float (&a)[16], int lane) {
   const bool hi = (lane & O) != 0;
 #pragma unroll
   for (int j = 0; j < NV / 2; ++j) {
@@ -219,15 +220,15 @@ __device__ __forceinline__ void rs_step(float (&a)[kHpt], int lane) {
     a[j] = MAX ? fmaxf(keep, got) : keep + got;
   }
 }
-// Afterwards lane l holds the warp-wide maximum (or sum) of value l.
+// Afterwards lane l holds the warp-wide maximum (or sum) of value l % 16.
 template <bool MAX>
-__device__ __forceinline__ float warp_reduce32(float (&a)[kHpt], int lane) {
-  rs_step<16, 32, MAX>(a, lane);
+__device__ __forceinline__ float warp_reduce16(float (&a)[16], int lane) {
   rs_step<8, 16, MAX>(a, lane);
   rs_step<4, 8, MAX>(a, lane);
   rs_step<2, 4, MAX>(a, lane);
   rs_step<1, 2, MAX>(a, lane);
-  return a[0];
+  const float other = __shfl_xor_sync(0xffffffffu, a[0], 16);
+  return MAX ? fmaxf(a[0], other) : a[0] + other;
 }
 
 // The tiles of list positions [ub, ue): entries, then window rows, each cut from its own start.
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
   const int hg = (blockIdx.x / splits) % groups;
   const int q = blockIdx.x / splits / groups;
   const int h0 = hg * kHT;
+  const Rows r = rows_of(p, q);  // (its loads overlap the set-up below)
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->qfull, 1);
@@ -273,18 +275,16 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     bars->abort = 0;
     tc::fence_mbar_init();
   }
-  for (int h = threadIdx.x; h < kHT; h += kThreads) bars->mref[h] = neg_inf();
+  for (int h = threadIdx.x; h < kHT; h += kThreads) bars->mref[h] = kNoMax;
   if (warp == 0) tc::tmem_alloc(&bars->tmem_base, kTmemCols);
+  const int ub = sp * rows_per_split;
+  const Tiles tiles(r.entries, r.window, ub, ub + rows_per_split);
+  const int nt = tiles.n;
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
   tc::griddep_launch_dependents();
-
-  const Rows r = rows_of(p, q);
-  const int ub = sp * rows_per_split;
-  const Tiles tiles(r.entries, r.window, ub, ub + rows_per_split);
-  const int nt = tiles.n;
 
   if (warp < 4) {
     // ------------------------------ MMA issuer ------------------------------
@@ -346,49 +346,84 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       }
     }
   } else if (warp < 4 + kSoft) {
-    tc::setmaxnreg_dec<64>();
+    tc::setmaxnreg_inc<96>();
 
     // ------------------------------ softmax ------------------------------
     const int quarter = warp & 3, hsel = (warp - 4) >> 2;  // TMEM lanes of this warp; heads [32 hsel, 32 hsel + 32)
     const int row = quarter * 32 + lane, st = threadIdx.x - 128;
     const uint32_t lanebase = (uint32_t)(quarter * 32) << 16;
     const float scale_log2 = p.scale * kLog2e;
+    // Heads are taken 16 at a time, to keep the registers of a thread few.
     float lw = 0.f;  // lane l: head 32 hsel + l's sum over this warp's rows, relative to the running maximum
+    unsigned char* prow = base + kOffP + row * 128;
     bool failed = false;
     for (int i = 0; i < nt; ++i) {
       const uint32_t ph = i & 1;
-      float sv[kHpt];
-      bool need = false;  // some score lies above its head's running maximum + 2^8 (or is the first one)
       // (block 0 landed long before S: this wait orders the converters' row flags before their use here)
       failed = !tc::warp_wait(&bars->vfull[0], ph, abort) || !tc::warp_wait(&bars->sfull, ph, abort);
       const bool valid = !failed && ((bars->rowok[i & 3][row >> 3] >> (4 * (row & 7))) & 1u);
-      auto load_scores = [&]() {
-        uint32_t v[kHpt];
-        tc::tmem_ld32(tmem + lanebase + kColS + kHpt * hsel, v);
+      const float bias = valid ? 0.f : neg_inf();
+      // scores of heads 16 x .. 16 x + 15 of this warp's in units of log2, -inf in rows that take no part
+      auto load_scores = [&](int x, float (&sv)[16]) {
+        uint32_t v[16];
+        tc::tmem_ld16(tmem + lanebase + kColS + kHpt * hsel + 16 * x, v);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < kHpt; ++h) sv[h] = valid ? __uint_as_float(v[h]) * scale_log2 : neg_inf();
+        for (int h = 0; h < 16; ++h) sv[h] = fmaf(__uint_as_float(v[h]), scale_log2, bias);
+      };
+      // ... relative to the running maxima
+      auto subtract_maxima = [&](int x, float (&sv)[16]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 m4 = *reinterpret_cast<const float4*>(bars->mref + kHpt * hsel + 16 * x + 4 * c);
+          sv[4 * c] -= m4.x;
+          sv[4 * c + 1] -= m4.y;
+          sv[4 * c + 2] -= m4.z;
+          sv[4 * c + 3] -= m4.w;
+        }
+      };
+      // P(i) against the running maxima (PV(i-1), the last reader of the buffer, has completed); returns the largest
+      // score relative to its head's maximum
+      auto write_p = [&]() -> float {
+        float top = neg_inf();
+#pragma unroll
+        for (int x = 0; x < kHpt / 16; ++x) {
+          float sv[16];
+          load_scores(x, sv);
+          subtract_maxima(x, sv);
+#pragma unroll
+          for (int h = 0; h < 16; h += 2) top = fmaxf(top, fmaxf(sv[h], sv[h + 1]));
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const int c = (kHpt / 8) * hsel + 2 * x + cc;  // 16-byte unit of the row: heads 8c .. 8c+7
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = pack_bf16x2(fast_exp2(sv[8 * cc + 2 * j]), fast_exp2(sv[8 * cc + 2 * j + 1]));
+            *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        return top;
       };
       if (!failed) tc::fence_after_sync();
-      load_scores();
-#pragma unroll
-      for (int c = 0; c < kHpt / 4; ++c) {
-        const float4 m4 = *reinterpret_cast<const float4*>(bars->mref + kHpt * hsel + 4 * c);
-        need |= sv[4 * c] > m4.x + kRescaleLog2;
-        need |= sv[4 * c + 1] > m4.y + kRescaleLog2;
-        need |= sv[4 * c + 2] > m4.z + kRescaleLog2;
-        need |= sv[4 * c + 3] > m4.w + kRescaleLog2;
-      }
-      // one vote for "nobody needs new maxima and nobody failed", the usual case
-      if (tc::named_bar_or(1, 32 * kSoft, need || failed || *abort)) {
+      const float top = i == 0 ? INFINITY : write_p();  // (the first tile sets the maxima in any case)
+      // One vote for "no score lies above its head's running maximum + 2^8 and nobody failed", the usual case: P
+      // stands.  Otherwise new maxima, rescaled accumulators, and P again.
+      if (tc::named_bar_or(1, 32 * kSoft, top > kRescaleLog2 || failed || *abort)) {
         if (tc::named_bar_or(1, 32 * kSoft, failed || *abort)) { failed = true; break; }
-        bars->red[quarter][kHpt * hsel + lane] = warp_reduce32<true>(sv, lane);  // (the scores are read again below)
+#pragma unroll 1
+        for (int x = 0; x < kHpt / 16; ++x) {
+          float sv[16];
+          load_scores(x, sv);
+          const float m = warp_reduce16<true>(sv, lane);
+          if (lane < 16) bars->red[quarter][kHpt * hsel + 16 * x + lane] = m;
+        }
         tc::named_bar(1, 32 * kSoft);
         if (st < kHT) {
           const float mt = fmaxf(fmaxf(bars->red[0][st], bars->red[1][st]), fmaxf(bars->red[2][st], bars->red[3][st]));
           const float mo = bars->mref[st];
-          const bool grow = mt > mo + kRescaleLog2;  // -inf + 2^8 = -inf: any first score
-          bars->alpha[st] = grow ? (mo == neg_inf() ? 0.f : fast_exp2(mo - mt)) : 1.f;
+          const bool grow = mt > mo + kRescaleLog2;
+          bars->alpha[st] = grow ? fast_exp2(mo - mt) : 1.f;
           if (grow) bars->mref[st] = mt;
         }
         tc::named_bar(1, 32 * kSoft);
@@ -397,45 +432,39 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
           // O^T holds the sums up to tile i-1 (PV(i-1) was issued before QK(i), whose commit has arrived)
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int b = 0; b < kBlocks; ++b) {
-            const uint32_t ta = tmem + lanebase + kColO + b * kHT + kHpt * hsel;
-            uint32_t v[kHpt];
-            tc::tmem_ld32(ta, v);
+          for (int part = 0; part < kBlocks * (kHpt / 16); ++part) {
+            const int hh = kHpt * hsel + 16 * (part & 1);
+            const uint32_t ta = tmem + lanebase + kColO + (part >> 1) * kHT + hh;
+            uint32_t v[16];
+            tc::tmem_ld16(ta, v);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < kHpt; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * bars->alpha[kHpt * hsel + h]);
-            tc::tmem_st32(ta, v);
+            for (int h = 0; h < 16; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * bars->alpha[hh + h]);
+            tc::tmem_st16(ta, v);
           }
           tc::tmem_st_wait();
         }
-        load_scores();
+        write_p();
       }
       tc::fence_before_sync();
-      // P(i): PV(i-1), the last reader of the buffer, has completed
-      unsigned char* prow = base + kOffP + row * 128;
-#pragma unroll
-      for (int cc = 0; cc < kHpt / 8; ++cc) {
-        const int c = (kHpt / 8) * hsel + cc;  // 16-byte unit of the row: heads 8c .. 8c+7
-        const float4 ma = *reinterpret_cast<const float4*>(bars->mref + c * 8);
-        const float4 mb = *reinterpret_cast<const float4*>(bars->mref + c * 8 + 4);
-        const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int h = cc * 8 + 2 * j;
-          const float m0 = mm[2 * j], m1 = mm[2 * j + 1];
-          const float p0 = (m0 == neg_inf()) ? 0.f : fast_exp2(sv[h] - m0);
-          const float p1 = (m1 == neg_inf()) ? 0.f : fast_exp2(sv[h + 1] - m1);
-          w[j] = pack_bf16x2(p0, p1);
-          sv[h] = bf16_lo(w[j]);  // exactly what PV multiplies
-          sv[h + 1] = bf16_hi(w[j]);
-        }
-        *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->pfull);
-      lw += warp_reduce32<false>(sv, lane);
+      // the row sums of exactly what PV multiplies, read back from this thread's own row
+#pragma unroll 1
+      for (int x = 0; x < kHpt / 16; ++x) {
+        float sv[16];
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const int c = (kHpt / 8) * hsel + 2 * x + cc;
+          float f[8];
+          unpack8(*reinterpret_cast<const uint4*>(prow + ((c ^ (row & 7)) << 4)), f);
+#pragma unroll
+          for (int h = 0; h < 8; ++h) sv[8 * cc + h] = f[h];
+        }
+        const float t = warp_reduce16<false>(sv, lane);
+        if ((lane >> 4) == x) lw += t;
+      }
     }
     // ---- epilogue: O^T (channels x heads) and l ----
     bars->red[quarter][kHpt * hsel + lane] = lw;
@@ -445,49 +474,55 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     if (ok) {
       tc::fence_after_sync();
       const int dl = quarter * 32 + lane;  // channel within its block
-      float lv[kHpt];
+      // reciprocal row sums (unsplit queries), once per head; a sink logit joins the denominator here (base-2, against
+      // the head's running maximum), for split queries in the combine
+      if (splits == 1) {
+        if (st < kHT) {
+          float l = (bars->red[0][st] + bars->red[1][st]) + (bars->red[2][st] + bars->red[3][st]);
+          if (p.sink != nullptr && h0 + st < p.H && l > 0.f) l += fast_exp2(p.sink[h0 + st] * kLog2e - bars->mref[st]);
+          bars->alpha[st] = l > 0.f ? __fdividef(1.f, l) : 0.f;
+        }
+        tc::named_bar(1, 32 * kSoft);
+      }
+      const int rope0 = kC - p.rope_dims;
+      bf16* stage = reinterpret_cast<bf16*>(base + kOffKv);  // the last PV has read the tile
+      const long long part0 = ((long long)q * splits + sp) * p.H + h0;
+#pragma unroll 1
+      for (int part = 0; part < kBlocks * (kHpt / 16); ++part) {
+        const int b = part >> 1, hh = kHpt * hsel + 16 * (part & 1);
+        uint32_t v[16];
+        if (nt > 0) {
+          tc::tmem_ld16(tmem + lanebase + kColO + b * kHT + hh, v);
+          tc::tmem_ld_wait();
+        } else {
 #pragma unroll
-      for (int h = 0; h < kHpt; ++h) {
-        const int hh = kHpt * hsel + h;
-        lv[h] = (bars->red[0][hh] + bars->red[1][hh]) + (bars->red[2][hh] + bars->red[3][hh]);
+          for (int h = 0; h < 16; ++h) v[h] = 0u;
+        }
+        const int d = b * 128 + dl;
+        if (splits > 1) {
+          float* wo = ws_o + (part0 + hh) * kC + d;
+#pragma unroll
+          for (int h = 0; h < 16; ++h)
+            if (h0 + hh + h < p.H) wo[h * kC] = __uint_as_float(v[h]);
+          continue;
+        }
+        // output rotation by -t: channel d pairs with d ^ 1, the neighbouring lane; whole warps take the branch
+        const bool rot = p.rope_dims > 0 && b * 128 + quarter * 32 + 31 >= rope0;
+        float rc = 1.f, rs = 0.f;
+        if (rot && d >= rope0) {
+          float sn;
+          rope_cos_sin(r.t, (d - rope0) >> 1, p.rope_dims, p.rope_base, rc, sn);
+          rs = (d & 1) ? -sn : sn;
+        }
+#pragma unroll
+        for (int h = 0; h < 16; ++h) {
+          const float inv = bars->alpha[hh + h];
+          float o = inv != 0.f ? __uint_as_float(v[h]) * inv : 0.f;
+          if (rot) o = fmaf(o, rc, __shfl_xor_sync(0xffffffffu, o, 1) * rs);
+          stage[(hh + h) * kOutLd + d] = __float2bfloat16_rn(o);
+        }
       }
       if (splits == 1) {
-#pragma unroll
-        for (int h = 0; h < kHpt; ++h) {
-          const int hh = kHpt * hsel + h;
-          // a sink logit joins the denominator here (base-2, against the head's running maximum)
-          if (p.sink != nullptr && h0 + hh < p.H && lv[h] > 0.f)
-            lv[h] += fast_exp2(p.sink[h0 + hh] * kLog2e - bars->mref[hh]);
-          lv[h] = lv[h] > 0.f ? __fdividef(1.f, lv[h]) : 0.f;
-        }
-        const int rope0 = kC - p.rope_dims;
-        bf16* stage = reinterpret_cast<bf16*>(base + kOffKv);  // the last PV has read the tile
-#pragma unroll 1
-        for (int b = 0; b < kBlocks; ++b) {
-          uint32_t v[kHpt];
-          if (nt > 0) {
-            tc::tmem_ld32(tmem + lanebase + kColO + b * kHT + kHpt * hsel, v);
-            tc::tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int h = 0; h < kHpt; ++h) v[h] = 0u;
-          }
-          const int d = b * 128 + dl;
-          // output rotation by -t: channel d pairs with d ^ 1, the neighbouring lane; whole warps take the branch
-          const bool rot = p.rope_dims > 0 && b * 128 + quarter * 32 + 31 >= rope0;
-          float rc = 1.f, rs = 0.f;
-          if (rot && d >= rope0) {
-            float sn;
-            rope_cos_sin(r.t, (d - rope0) >> 1, p.rope_dims, p.rope_base, rc, sn);
-            rs = (d & 1) ? -sn : sn;
-          }
-#pragma unroll
-          for (int h = 0; h < kHpt; ++h) {
-            float o = lv[h] != 0.f ? __uint_as_float(v[h]) * lv[h] : 0.f;
-            if (rot) o = fmaf(o, rc, __shfl_xor_sync(0xffffffffu, o, 1) * rs);
-            stage[(kHpt * hsel + h) * kOutLd + d] = __float2bfloat16_rn(o);
-          }
-        }
         tc::named_bar(1, 32 * kSoft);
         bf16* out = p.out + ((long long)q * p.H + h0) * kC;
         const int nh = min(kHT, p.H - h0);
@@ -496,30 +531,14 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
           *reinterpret_cast<uint4*>(out + h * kC + x * 8) = *reinterpret_cast<const uint4*>(stage + h * kOutLd + x * 8);
         }
       } else {
-        const long long part = ((long long)q * splits + sp) * p.H + h0;
-        float* wo = ws_o + part * kC;
-#pragma unroll 1
-        for (int b = 0; b < kBlocks; ++b) {
-          uint32_t v[kHpt];
-          if (nt > 0) {
-            tc::tmem_ld32(tmem + lanebase + kColO + b * kHT + kHpt * hsel, v);
-            tc::tmem_ld_wait();
-          }
-#pragma unroll
-          for (int h = 0; h < kHpt; ++h) {
-            const int hh = kHpt * hsel + h;
-            if (h0 + hh < p.H) wo[hh * kC + b * 128 + dl] = nt > 0 ? __uint_as_float(v[h]) : 0.f;
-          }
-        }
         if (st < kHT && h0 + st < p.H) {
           const float l = (bars->red[0][st] + bars->red[1][st]) + (bars->red[2][st] + bars->red[3][st]);
-          ws_ml[part + st] = make_float2(l > 0.f ? bars->mref[st] : neg_inf(), l);
+          ws_ml[part0 + st] = make_float2(l > 0.f ? bars->mref[st] : neg_inf(), l);
         }
       }
     }
   } else {
     // ------------------------------ converters ------------------------------
-    tc::setmaxnreg_inc<88>();
     const int cw = warp - 4 - kSoft;
     const int row = 8 * cw + (lane >> 2), sub = lane & 3;    // row of the tile; group 4b + sub of block b
     const int n_groups = (kC - p.kv.rope_dims) / kFp4Group;  // groups held in 4 bits
@@ -538,15 +557,23 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       const int u = tiles.first(i) + row;
       return r.idx ? r.idx[u] : u;
     };
-    auto resolve = [&](int i, int e) -> int {
+    // The block that entry e lies in (paged), loaded but not looked at yet, and its cache row from it.
+    auto block_of = [&](int e) -> int {
+      if (!p.kv.bt || e < 0 || e >= p.N) return 0;
+      const unsigned int j = div_by(e, p.rpb);
+      return j < p.kv.bt_stride ? p.kv.bt[r.req * p.kv.bt_stride + j] : -1;
+    };
+    auto resolve = [&](int i, int e, int blk) -> int {
       if (p.check && sub == 0 && r.idx && i < tiles.na && row < tiles.rows(i)) {
         const unsigned int k = entry_check(e, r.t, p.rate, p.N);
         if (k) atomicOr(&g_mqa_fp4_error, k << 1);
       }
       if (e < 0 || e >= p.N) return -1;
-      const int x = (int)kv_row32(p.kv, r.req, e);
+      long long x = p.kv.bt ? (blk < 0 ? -1ll : (long long)blk * p.kv.rpb + (e - (int)(div_by(e, p.rpb) * p.rpb.d)))
+                            : (e < p.kv.seq_rows ? r.req * p.kv.seq_rows + e : -1ll);
+      if (x >= p.kv.n_rows) x = -1;
       if (p.check && x < 0) atomicOr(&g_mqa_fp4_error, kIdxBlock << 1);
-      return x;
+      return (int)x;
     };
     // The codes of this thread's group of block b of cache row x, in the order of its stores (halves swapped in the
     // second chunk).
@@ -572,60 +599,62 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       copy_row(i, 7, p.kv.rope + (x >= 0 ? x * p.kv.ld_rope : 0ll), x >= 0);
       tc::cp_async_commit();
     };
-    // Cache rows of the tile being converted and of the next one, the entry of the one after: an index, its block and
-    // its row are dependent loads, each given a tile's time.
-    const int e0 = entry_of(0), e1 = entry_of(1);
-    int x = resolve(0, e0), xn = resolve(1, e1);
-    int e_next = entry_of(2);
+    // An entry's index, its block and its row are dependent loads, each given a tile's time: x is the cache row of the
+    // tile being converted, e1 and b1 entry and block of the next one, e2 the entry of the one after.
+    const int e0 = entry_of(0);
+    int e1 = entry_of(1), e2 = entry_of(2);
+    int x = resolve(0, e0, block_of(e0));
+    int b1 = block_of(e1);
     if (rope64 && tiles.na > 0) copy_rope(0, x);
-    // Widen this thread's group of block b.
-    auto widen = [&](int x, int b, const uint4& v, uint32_t scale_word, uint4 (&o)[4]) {
-      const int g = 4 * b + sub;
-      if (g < n_groups) {
-        e2m1x32_to_bf16(v, (int)((scale_word >> (8 * sub)) & 255u) - 127, o);
-      } else if (!rope64) {
-#pragma unroll
-        for (uint32_t w = 0; w < 4; ++w)
-          o[w] = x >= 0 ? *reinterpret_cast<const uint4*>(p.kv.rope + x * p.kv.ld_rope + (g - n_groups) * 32 +
-                                                          ((2 * chunk) ^ w) * 8)
-                        : make_uint4(0u, 0u, 0u, 0u);
-      }
+    // Widen this thread's group of block b (one that is not held in 4 bits: its codes are zeros).
+    auto widen = [&](int b, const uint4& v, uint32_t scale_word, uint4 (&o)[4]) {
+      e2m1x32_to_bf16(v, (int)((scale_word >> (8 * sub)) & 255u) - 127, o);
     };
-    bool okw = true;
-    // Once block b is free, store a widened group and signal the block.
+    // Store a widened group of block b and signal the block.
     auto put = [&](int i, int b, const uint4 (&o)[4]) {
-      if (!okw || !(okw = tc::warp_wait(&bars->vempty[b], (i & 1) ^ 1, abort))) return;
-      if (4 * b + sub < n_groups || !rope64) {
-        unsigned char* d = row_of(i, 2 * b + chunk);
+      const int g = 4 * b + sub;
+      unsigned char* d = row_of(i, 2 * b + chunk);
+      if (g < n_groups) {
 #pragma unroll
         for (uint32_t w = 0; w < 4; ++w) *reinterpret_cast<uint4*>(d + (((unit0 ^ w) ^ sw) << 4)) = o[w];
+      } else if (!rope64) {  // other numbers of rotary channels: copied here
+        const bf16* src = p.kv.rope + (x >= 0 ? x * p.kv.ld_rope + (g - n_groups) * 32 : 0ll);
+#pragma unroll 1
+        for (uint32_t w = 0; w < 4; ++w)
+          tc::cp_async16(tc::smem_u32(d) + (((4 * (sub & 1) + w) ^ sw) << 4), src + w * 8, x >= 0 ? 16 : 0);
+        tc::cp_async_commit();
       }
-      if (b == kBlocks - 1) tc::cp_async_wait<0>();  // the last chunk, under way since the last tile
+      if (b == kBlocks - 1 || !rope64) tc::cp_async_wait<0>();  // (64 rotary channels: under way since the last tile)
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->vfull[b]);
     };
+    bool okw = true;
     int i = 0;
     for (; okw && i < tiles.na; ++i) {
+      const uint32_t ph = i & 1;
       const uint32_t mask = __ballot_sync(0xffffffffu, x >= 0);
       if (lane == 0) bars->rowok[i & 3][cw] = mask;
-      uint4 o0[4], o1[4], o2[4];
+      uint4 oa[4], ob[4];
       const uint4 sc = fetch_scales(x);
       const uint4 v0 = fetch(x, 0), v1 = fetch(x, 1), v2 = fetch(x, 2), v3 = fetch(x, 3);
-      const int x2 = resolve(i + 2, e_next);
-      e_next = entry_of(i + 3);
-      widen(x, 0, v0, sc.x, o0);
-      widen(x, 1, v1, sc.y, o1);
-      widen(x, 2, v2, sc.z, o2);
-      put(i, 0, o0);
-      widen(x, 3, v3, sc.w, o0);
-      put(i, 1, o1);
-      put(i, 2, o2);
-      put(i, 3, o0);
-      // PV of tile i-1 has released every block here: its buffer of the last chunk takes tile i+1's
-      if (rope64 && i + 1 < tiles.na) copy_rope(i + 1, xn);
-      x = xn;
-      xn = x2;
+      widen(0, v0, sc.x, oa);
+      widen(1, v1, sc.y, ob);
+      if (!(okw = tc::warp_wait(&bars->vempty[0], ph ^ 1, abort))) break;
+      put(i, 0, oa);
+      widen(2, v2, sc.z, oa);
+      if (!(okw = tc::warp_wait(&bars->vempty[1], ph ^ 1, abort))) break;
+      put(i, 1, ob);
+      widen(3, v3, sc.w, ob);
+      if (!(okw = tc::warp_wait(&bars->vempty[kBlocks - 1], ph ^ 1, abort))) break;
+      put(i, 2, oa);
+      put(i, 3, ob);
+      // PV of tile i-1 has released its buffer of the last chunk: it takes tile i+1's
+      x = resolve(i + 1, e1, b1);
+      if (rope64 && i + 1 < tiles.na) copy_rope(i + 1, x);
+      e1 = e2;
+      b1 = block_of(e1);
+      e2 = entry_of(i + 3);
     }
     for (; okw && i < nt; ++i) {  // window rows
       const uint32_t ph = i & 1;
@@ -699,8 +728,10 @@ MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms) {
   return pl;
 }
 
-cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, cudaStream_t stream) {
-  if (p.Tq == 0) return cudaSuccess;
+cudaError_t launch_mqa_fp4(const MqaFp4Problem& problem, const MqaPlan& pl, void* ws, cudaStream_t stream) {
+  if (problem.Tq == 0) return cudaSuccess;
+  MqaFp4Problem p = problem;
+  p.rpb = fast_div((uint32_t)p.kv.rpb);
   float* ws_o = reinterpret_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)p.Tq * pl.splits * p.H * p.kv.c);
   cudaError_t e;

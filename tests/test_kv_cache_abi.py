@@ -104,11 +104,11 @@ def test_attend_refusals(lib):
     shape = dict(c=512, m=4, m_hca=128, topk=1024, n_idx_heads=64, d_idx=128, n_heads=64, n_win=128, scale=512 ** -0.5,
                  rope_dims=64, rope_base=1e4, norm_eps=1e-6)
     cfg = lambda **kw: lib.make_cfg(SimpleNamespace(**dict(shape, **kw)))  # noqa: E731
-    need = lib.sparse_mqa_attend_fp4_workspace(cfg(), 4, 100, 0)
+    need = lib.sparse_mqa_attend_fp4_workspace(cfg(), 4, 8192, 0)
     assert 0 < need < lib.SIZE_MAX and need % 256 == 0
 
     def call(**kw):
-        a = dict(q=FAKE, d=desc(lib), N=100, idx=None, k=0, rate=4, win=FAKE, ws_=128 * 512, W=128, pos=FAKE, req=None, Tq=4,
+        a = dict(q=FAKE, d=desc(lib), N=8192, idx=None, k=0, rate=4, win=FAKE, ws_=128 * 512, W=128, pos=FAKE, req=None, Tq=4,
                  cfg=cfg(), sink=None, rot=0, out=FAKE, ws=FAKE, nb=1 << 30)
         a.update(kw)
         return lib._mqa_fp4(a["q"], ctypes.byref(a["d"]) if a["d"] else None, a["N"], a["idx"], a["k"], a["rate"], a["win"],
