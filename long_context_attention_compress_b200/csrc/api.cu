@@ -1462,6 +1462,7 @@ int kv_cache_gather(const hca_kv_cache* cache, int B, int n_out, const int32_t* 
   return HCA_OK;
 }
 
+constexpr int kMaxFp4Queries = 1 << 20;
 // The layer fields that the attention over FP4 entries reads.
 static int check_fp4_cfg(const hca_layer_cfg* cfg, const char* who) {
   CHECK(cfg != nullptr, HCA_ERR_INVALID_ARG, "%s: cfg null", who);
@@ -1488,16 +1489,23 @@ static MqaFp4Problem fp4_problem(const hca_layer_cfg* cfg, int Tq, int N, const 
 }
 
 // The plan takes a window to be there, so that the size of the workspace does not depend on it.
-static MqaPlan fp4_plan(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
-  return plan_mqa_fp4(fp4_problem(cfg, Tq, N, n_idx ? reinterpret_cast<const int32_t*>(1) : nullptr, n_idx,
-                                  reinterpret_cast<const hca_bf16*>(1)),
-                      device_sm_count());
+static MqaPlan fp4_plan(const hca_layer_cfg* cfg, int Tq, int N, int n_idx, bool q_req) {
+  MqaFp4Problem p = fp4_problem(cfg, Tq, N, n_idx ? reinterpret_cast<const int32_t*>(1) : nullptr, n_idx,
+                                reinterpret_cast<const hca_bf16*>(1));
+  p.q_req = q_req ? reinterpret_cast<const int32_t*>(1) : nullptr;
+  return plan_mqa_fp4(p, device_sm_count());
+}
+// Whether the queries name their requests or not.
+static size_t fp4_ws(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
+  if (Tq == 0) return 0;
+  return round256(std::max(fp4_plan(cfg, Tq, N, n_idx, false).ws_bytes, fp4_plan(cfg, Tq, N, n_idx, true).ws_bytes));
 }
 
 size_t sparse_mqa_attend_fp4_workspace(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
-  if (check_fp4_cfg(cfg, "sparse_mqa_attend_fp4") != HCA_OK || Tq < 0 || N < 0 || n_idx < 0 || n_idx > 4096)
+  if (check_fp4_cfg(cfg, "sparse_mqa_attend_fp4") != HCA_OK || Tq < 0 || Tq > kMaxFp4Queries || N < 0 || n_idx < 0 ||
+      n_idx > 4096)
     return (size_t)-1;
-  return Tq == 0 ? 0 : round256(fp4_plan(cfg, Tq, N, n_idx).ws_bytes);
+  return fp4_ws(cfg, Tq, N, n_idx);
 }
 
 int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, const int32_t* idx, int n_idx, int rate,
@@ -1514,7 +1522,8 @@ int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, c
   CHECK(cache->c == cfg->c, HCA_ERR_INVALID_ARG, "%s: cache c=%d, cfg c=%d", who, cache->c, cfg->c);
   CHECK(aligned16(cache->scales) && cache->ld_scales % 16 == 0, HCA_ERR_INVALID_ARG,
         "%s: cache scales not 16-byte aligned, or ld_scales %lld not a multiple of 16", who, cache->ld_scales);
-  CHECK(Tq >= 0 && N >= 0 && rate >= 1, HCA_ERR_INVALID_ARG, "%s: Tq=%d N=%d rate=%d", who, Tq, N, rate);
+  CHECK(Tq >= 0 && Tq <= kMaxFp4Queries && N >= 0 && rate >= 1, HCA_ERR_INVALID_ARG, "%s: Tq=%d (at most %d) N=%d rate=%d",
+        who, Tq, kMaxFp4Queries, N, rate);
   CHECK(idx ? (n_idx > 0 && n_idx <= 4096) : n_idx == 0, HCA_ERR_INVALID_ARG, "%s: n_idx=%d", who, n_idx);
   CHECK(q_req || Tq <= cache->n_req, HCA_ERR_INVALID_ARG, "%s: %d queries for %d requests without q_req", who, Tq,
         cache->n_req);
@@ -1524,7 +1533,7 @@ int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, c
   CHECK(!rotate_out || (cfg->rope_dims > 0 && cfg->rope_dims % 8 == 0 && cfg->rope_dims <= cfg->c &&
                         cfg->rope_dims <= 256 && cfg->rope_base > 0.f),
         HCA_ERR_INVALID_ARG, "%s: rotate_out with rope_dims=%d rope_base=%g", who, cfg->rope_dims, cfg->rope_base);
-  const size_t need = Tq == 0 ? 0 : round256(fp4_plan(cfg, Tq, N, idx ? n_idx : 0).ws_bytes);
+  const size_t need = fp4_ws(cfg, Tq, N, idx ? n_idx : 0);
   CHECK(ws_bytes >= need, HCA_ERR_WORKSPACE, "%s: workspace %zu < %zu", who, ws_bytes, need);
   if (Tq == 0) return HCA_OK;
   CHECK_PTR(q, "sparse_mqa_attend_fp4: q");
@@ -1549,7 +1558,7 @@ int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, c
   p.rope_base = cfg->rope_base;
   p.out = reinterpret_cast<bf16*>(out);
   p.check = debug_checks() ? 1 : 0;
-  CUDA_TRY(launch_mqa_fp4(p, fp4_plan(cfg, Tq, N, idx ? n_idx : 0), ws, as_stream(stream)), who);
+  CUDA_TRY(launch_mqa_fp4(p, fp4_plan(cfg, Tq, N, idx ? n_idx : 0, q_req != nullptr), ws, as_stream(stream)), who);
   return HCA_OK;
 }
 

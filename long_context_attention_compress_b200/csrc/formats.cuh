@@ -2,7 +2,6 @@
 // power-of-two scale per 32 channels) and FP8 (E4M3 elements, one f32 scale per 64 channels).
 #pragma once
 
-#include <cuda_fp16.h>
 #include <string.h>
 
 #include "common.cuh"
@@ -71,48 +70,25 @@ __device__ __forceinline__ uint32_t prmt_raw(uint32_t a, uint32_t b, uint32_t se
   return d;
 }
 // A whole MXFP4 block: 32 codes (16 bytes) times 2^X -> 32 bf16 as four 16-byte words, for scale bytes below 255.
-// Straight-line code for every X: both multiplications are exact, or round to the bf16 subnormal or infinity that the
-// value has (2^-127 itself is a subnormal factor, which both take).  The byte-table form above is bound by the ALU
-// pipe (14 half-rate instructions per 8 codes), so two of the four words go through the conversion instruction
-// instead (E2M1 -> f16 -> f32, times 2^X, -> bf16), whose middle steps run on the FMA pipe.
+// The same byte tables, in straight-line code for every X: the multiplication is exact, or rounds to the bf16
+// subnormal or infinity that the value has (2^-127 itself is a subnormal factor, which it takes).  14 half-rate and 4
+// multiply instructions per 8 codes; the conversion instruction (E2M1 -> f16 -> f32, times 2^X, -> bf16) takes 24,
+// and mixing the two to use both pipes was slower in the attention, which is bound by issue slots.
 __device__ __forceinline__ void e2m1x32_to_bf16(const uint4& w, int X, uint4* o) {
+  constexpr uint32_t kHiLo = 0x3F3F3F00u, kHiHi = 0x40404040u, kLoLo = 0xC0800000u, kLoHi = 0xC0804000u;
   const uint32_t e = (uint32_t)(127 + X);
-  const float scf = __uint_as_float(e ? e << 23 : 0x00400000u);
   const uint32_t sb = e ? e << 7 : 0x0040u, sbits = sb | (sb << 16);  // 2^X twice, as bf16
   const uint32_t c[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t t[4];
-    if (i & 1) {
-      constexpr uint32_t kHiLo = 0x3F3F3F00u, kHiHi = 0x40404040u, kLoLo = 0xC0800000u, kLoHi = 0xC0804000u;
-      const uint32_t x = c[i], x4 = x << 4, m = x & 0x77777777u, mh = m >> 16;
-      const uint32_t h0 = prmt_raw(kHiLo, kHiHi, m) | (prmt_raw(x4, x, 0x5140u) & 0x80808080u);
-      const uint32_t h1 = prmt_raw(kHiLo, kHiHi, mh) | (prmt_raw(x4, x, 0x7362u) & 0x80808080u);
-      const uint32_t l0 = prmt_raw(kLoLo, kLoHi, m), l1 = prmt_raw(kLoLo, kLoHi, mh);
-      t[0] = prmt_raw(l0, h0, 0x5140u);
-      t[1] = prmt_raw(l0, h0, 0x7362u);
-      t[2] = prmt_raw(l1, h1, 0x5140u);
-      t[3] = prmt_raw(l1, h1, 0x7362u);
+    const uint32_t x = c[i], x4 = x << 4, m = x & 0x77777777u, mh = m >> 16;
+    const uint32_t h0 = prmt_raw(kHiLo, kHiHi, m) | (prmt_raw(x4, x, 0x5140u) & 0x80808080u);
+    const uint32_t h1 = prmt_raw(kHiLo, kHiHi, mh) | (prmt_raw(x4, x, 0x7362u) & 0x80808080u);
+    const uint32_t l0 = prmt_raw(kLoLo, kLoHi, m), l1 = prmt_raw(kLoLo, kLoHi, mh);
+    uint32_t t[4] = {prmt_raw(l0, h0, 0x5140u), prmt_raw(l0, h0, 0x7362u), prmt_raw(l1, h1, 0x5140u),
+                     prmt_raw(l1, h1, 0x7362u)};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t[k]) : "r"(t[k]), "r"(sbits));
-    } else {
-      uint32_t h[4];
-      asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-          "mov.b32 {a, b, c, d}, %4;\n\t"
-          "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-          "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-          "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-          "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-          : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-          : "r"(c[i]));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        __half2 v;
-        memcpy(&v, &h[k], 4);
-        const float2 f = __half22float2(v);
-        t[k] = pack_bf16x2(f.x * scf, f.y * scf);
-      }
-    }
+    for (int k = 0; k < 4; ++k) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t[k]) : "r"(t[k]), "r"(sbits));
     o[i] = make_uint4(t[0], t[1], t[2], t[3]);
   }
 }

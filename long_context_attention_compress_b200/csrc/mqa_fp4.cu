@@ -190,13 +190,13 @@ constexpr uint32_t kOffBars = kOffR2 + kKvChunk;
 constexpr uint32_t kR2Delta = kOffR2 - (kOffKv + 7 * kKvChunk);  // second buffer of the last chunk, after the first
 constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
-constexpr float kNoMax = -1e30f;                      // running maximum of a head without a score yet (finite: -inf - kNoMax = -inf)
+constexpr float kNoMax = -1e30f;                      // running maximum of a head without a score yet
 constexpr int kHpt = kHT * 4 / kSoft;                // heads per softmax thread (32)
 constexpr int kOutLd = kC + 8;                       // staged output row (bf16), padded against bank conflicts
 
 struct __align__(16) Bars {
   float red[4][kHT];
-  float mref[kHT];
+  float nref[kHT];      // running maxima, negated
   float alpha[kHT];
   uint64_t qfull, vfull[kBlocks], vempty[kBlocks], sfull, pfull, odone, drain;
   uint32_t rowok[4][kConv];  // [tile % 4][converter warp]: bit 4 j is set where row j of the warp's eight takes part
@@ -207,47 +207,96 @@ constexpr size_t kSmemBytes = 1024 + kOffBars + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kHT * kOutLd * 2 <= kKvBytes, "staged output fits in the tile buffer");
 
-// One reduce-scatter step over lane bit O: of the NV values held, keep the half selected by the bit and fold in the
+// One reduce-scatter step over lane bit O: of the NV values held, keep the half selected by the bit and add the
 // partner's copy of that half.
-template <int O, int NV, bool MAX>
-__device__ __forceinline__ void rs_step(float (&a)[16], int lane) {
+template <int O, int NV>
+__device__ __forceinline__ void rs_sum_step(float (&a)[16], int lane) {
   const bool hi = (lane & O) != 0;
 #pragma unroll
   for (int j = 0; j < NV / 2; ++j) {
     const float send = hi ? a[j] : a[j + NV / 2];
     const float keep = hi ? a[j + NV / 2] : a[j];
-    const float got = __shfl_xor_sync(0xffffffffu, send, O);
-    a[j] = MAX ? fmaxf(keep, got) : keep + got;
+    a[j] = keep + __shfl_xor_sync(0xffffffffu, send, O);
   }
 }
-// Afterwards lane l holds the warp-wide maximum (or sum) of value l % 16.
-template <bool MAX>
-__device__ __forceinline__ float warp_reduce16(float (&a)[16], int lane) {
-  rs_step<8, 16, MAX>(a, lane);
-  rs_step<4, 8, MAX>(a, lane);
-  rs_step<2, 4, MAX>(a, lane);
-  rs_step<1, 2, MAX>(a, lane);
-  const float other = __shfl_xor_sync(0xffffffffu, a[0], 16);
-  return MAX ? fmaxf(a[0], other) : a[0] + other;
+// Afterwards lane l holds the warp-wide sum of value l % 16.
+__device__ __forceinline__ float warp_sum16(float (&a)[16], int lane) {
+  rs_sum_step<8, 16>(a, lane);
+  rs_sum_step<4, 8>(a, lane);
+  rs_sum_step<2, 4>(a, lane);
+  rs_sum_step<1, 2>(a, lane);
+  return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 16);
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// The tiles of list positions [ub, ue): entries, then window rows, each cut from its own start.
-struct Tiles {
-  int a0, a1, w0, w1, na, n;
-  __device__ __forceinline__ Tiles(int entries, int window, int ub, int ue) {
-    a0 = min(ub, entries);
-    a1 = min(ue, entries);
-    w0 = min(max(ub - entries, 0), window);
-    w1 = min(max(ue - entries, 0), window);
-    na = (a1 - a0 + kRowsT - 1) / kRowsT;
-    n = na + (w1 - w0 + kRowsT - 1) / kRowsT;
+// What a CTA attends to.  Without packing: one query and up to 64 of its heads.  Packed (dense entries, at most 32
+// heads, queries that name their requests): the 64 columns of the MMA are the heads of G = 64 / H consecutive queries
+// (32 at most), so that the queries of a chunk share the rows that are widened for them.  The group is cut into runs
+// of neighbouring queries of one request with positions at most kRunStep apart; a run's rows are the union of its
+// queries', and each column masks the rows that its query does not see.
+constexpr int kRunStep = 4;
+struct Run {
+  int j0, j1;         // queries of the group
+  int req;
+  int entries;        // cache entries (or selected slots)
+  int tok0, window;   // window tokens tok0 .. tok0 + window - 1
+  int na, n;          // tiles of entries, and all
+  int least;          // entries that every query of the run sees
+};
+template <bool PACK>
+struct Group {
+  int n;              // queries
+  int t, vis, req;    // this lane's query: position (-1: a padding query), entries, request
+  unsigned int starts;
+  const int32_t* idx;
+  __device__ __forceinline__ Group(const MqaFp4Problem& p, int q0, int g, int lane) {
+    n = PACK ? min(g, p.Tq - q0) : 1;
+    const int j = PACK ? min(lane, n - 1) : 0;
+    t = p.q_pos[q0 + j];
+    req = p.q_req ? p.q_req[q0 + j] : q0 + j;
+    idx = p.idx ? p.idx + (long long)q0 * p.n_idx : nullptr;
+    if (t < 0 || req < 0 || req >= p.kv.n_req) t = -1;
+    vis = t < 0 || p.N <= 0 ? 0 : (idx ? p.n_idx : n_visible(t, p.rate, p.N));
+    starts = 1u;
+    if (PACK) {
+      const int t1 = __shfl_up_sync(0xffffffffu, t, 1), r1 = __shfl_up_sync(0xffffffffu, req, 1);
+      starts = __ballot_sync(0xffffffffu, lane == 0 || r1 != req || (t1 < 0) != (t < 0) || t - t1 > kRunStep ||
+                                              t1 - t > kRunStep);
+    }
   }
-  __device__ __forceinline__ int first(int i) const { return i < na ? a0 + i * kRowsT : w0 + (i - na) * kRowsT; }
-  __device__ __forceinline__ int rows(int i) const { return min(kRowsT, (i < na ? a1 : w1) - first(i)); }
+  // (all lanes of a warp)
+  __device__ __forceinline__ Run run(const MqaFp4Problem& p, int j0, int lane) const {
+    Run r;
+    r.j0 = j0;
+    r.j1 = 1;
+    int tmin = t, tmax = t;
+    r.entries = r.least = vis;
+    r.req = req;
+    if (PACK) {
+      const unsigned int later = j0 < 31 ? starts >> (j0 + 1) : 0u;
+      r.j1 = min(n, later ? j0 + __ffs(later) : 32);
+      const bool in = lane >= r.j0 && lane < r.j1;
+      r.entries = __reduce_max_sync(0xffffffffu, in ? vis : 0);
+      r.least = __reduce_min_sync(0xffffffffu, in ? vis : 0x7fffffff);
+      tmin = __reduce_min_sync(0xffffffffu, in ? t : 0x7fffffff);
+      tmax = __reduce_max_sync(0xffffffffu, in ? t : -1);
+      r.req = __shfl_sync(0xffffffffu, req, j0);
+    }
+    r.tok0 = max(0, tmin - p.n_win + 1);
+    r.window = tmax >= 0 && p.win ? tmax - r.tok0 + 1 : 0;
+    r.na = (r.entries + kRowsT - 1) / kRowsT;
+    r.n = r.na + (r.window + kRowsT - 1) / kRowsT;
+    return r;
+  }
 };
 
+template <bool PACK>
 __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
-                                                                 MqaFp4Problem p, int splits, int rows_per_split,
+                                                                 MqaFp4Problem p, int G, int splits,
                                                                  float* __restrict__ ws_o,
                                                                  float2* __restrict__ ws_ml) {
   extern __shared__ unsigned char smem_raw[];
@@ -255,12 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
   Bars* bars = reinterpret_cast<Bars*>(base + kOffBars);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (p.H + kHT - 1) / kHT;
   const int sp = blockIdx.x % splits;
-  const int hg = (blockIdx.x / splits) % groups;
-  const int q = blockIdx.x / splits / groups;
-  const int h0 = hg * kHT;
-  const Rows r = rows_of(p, q);  // (its loads overlap the set-up below)
+  const int heads = PACK ? 1 : (p.H + kHT - 1) / kHT;  // groups of 64 heads
+  const int h0 = PACK ? 0 : ((blockIdx.x / splits) % heads) * kHT;
+  const int q0 = blockIdx.x / splits / heads * (PACK ? G : 1);
+  const Group<PACK> grp(p, q0, G, lane);  // (its loads overlap the set-up below)
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->qfull, 1);
@@ -275,16 +323,84 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     bars->abort = 0;
     tc::fence_mbar_init();
   }
-  for (int h = threadIdx.x; h < kHT; h += kThreads) bars->mref[h] = kNoMax;
+  for (int h = threadIdx.x; h < kHT; h += kThreads) bars->nref[h] = -kNoMax;
   if (warp == 0) tc::tmem_alloc(&bars->tmem_base, kTmemCols);
-  const int ub = sp * rows_per_split;
-  const Tiles tiles(r.entries, r.window, ub, ub + rows_per_split);
-  const int nt = tiles.n;
+  // The group's tiles, run by run, entries before the window; this CTA takes those from ga to gb.
+  int total = 0;
+  for (int j = 0; j < grp.n;) {
+    const Run r = grp.run(p, j, lane);
+    total += r.n;
+    j = r.j1;
+  }
+  const int each = total / splits, extra = total - each * splits;  // the first `extra` CTAs take one more
+  const int ga = sp * each + min(sp, extra), nt = each + (sp < extra ? 1 : 0), gb = ga + nt;
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
   tc::griddep_launch_dependents();
+
+  // ---- epilogue pieces, shared by the softmax and converter warps ----
+  // Row of the partial states (or, unsplit, of the output) of column lane and of column 32 + lane; -1: not an output.
+  auto column_row = [&](int c) -> int {
+    if (PACK) {
+      const int j = c / p.H;
+      return j < grp.n ? ((q0 + j) * splits + sp) * p.H + (c - j * p.H) : -1;
+    }
+    return h0 + c < p.H ? (q0 * splits + sp) * p.H + h0 + c : -1;
+  };
+  const int quarter = warp & 3;  // TMEM lanes of this warp
+  const uint32_t lanebase = (uint32_t)(quarter * 32) << 16;
+  bf16* stage = reinterpret_cast<bf16*>(base + kOffKv);  // the last PV has read the tile
+  // Channels [128 b + 32 quarter, +32) of columns [16 x, 16 x + 16): partial states to memory, or the finished output,
+  // turned by (rc, rs), to its staging.
+  auto store_part = [&](int b, int x, float rc, float rs) {
+    uint32_t v[16];
+    if (nt > 0) {
+      tc::tmem_ld16(tmem + lanebase + kColO + b * kHT + 16 * x, v);
+      tc::tmem_ld_wait();
+    } else {
+#pragma unroll
+      for (int h = 0; h < 16; ++h) v[h] = 0u;
+    }
+    const int d = b * 128 + quarter * 32 + lane;
+    if (PACK || splits > 1) {
+      const int mine = column_row(32 * (x >> 1) + lane);
+#pragma unroll
+      for (int h = 0; h < 16; ++h) {
+        const int to = __shfl_sync(0xffffffffu, mine, 16 * (x & 1) + h);
+        if (to >= 0) ws_o[(long long)to * kC + d] = __uint_as_float(v[h]);
+      }
+      return;
+    }
+    const bool rot = p.rope_dims > 0 && b * 128 + quarter * 32 + 31 >= kC - p.rope_dims;  // (of whole warps)
+#pragma unroll
+    for (int h = 0; h < 16; ++h) {
+      const float inv = bars->alpha[16 * x + h];
+      float o = inv != 0.f ? __uint_as_float(v[h]) * inv : 0.f;
+      if (rot) o = fmaf(o, rc, __shfl_xor_sync(0xffffffffu, o, 1) * rs);
+      stage[(16 * x + h) * kOutLd + d] = __float2bfloat16_rn(o);
+    }
+  };
+  // After every softmax and converter warp has staged its parts: the output's rows, 16 bytes a thread.
+  auto copy_out = [&]() {
+    if (PACK || splits > 1) return;
+    tc::named_bar(3, 32 * (kSoft + kConv));
+    bf16* out = p.out + ((long long)q0 * p.H + h0) * kC;
+    const int nh = min(kHT, p.H - h0);
+    for (int u = threadIdx.x - 128; u < nh * (kC / 8); u += 32 * (kSoft + kConv)) {
+      const int h = u / (kC / 8), x = u % (kC / 8);
+      *reinterpret_cast<uint4*>(out + h * kC + x * 8) = *reinterpret_cast<const uint4*>(stage + h * kOutLd + x * 8);
+    }
+  };
+  // Every softmax and converter warp comes here once its loop has ended: true when all of them may read O^T and the
+  // reciprocal row sums.
+  auto all_done = [&](bool ok) -> bool {
+    if (ok && nt > 0) ok = tc::warp_wait(&bars->odone, (nt - 1) & 1, abort);
+    ok = !tc::named_bar_or(2, 32 * (kSoft + kConv), !ok || *abort);
+    if (ok) tc::fence_after_sync();
+    return ok;
+  };
 
   if (warp < 4) {
     // ------------------------------ MMA issuer ------------------------------
@@ -293,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       const bool lead = tc::elect_one();
       if (lead) {
         tc::mbar_arrive_expect_tx(&bars->qfull, kQBytes);
-        for (int ch = 0; ch < 8; ++ch) tc::tma_load_3d(base + kOffQ + ch * kQChunk, &tm_q, &bars->qfull, ch * 64, h0, q);
+        for (int ch = 0; ch < 8; ++ch) tc::tma_load_3d(base + kOffQ + ch * kQChunk, &tm_q, &bars->qfull, ch * 64, PACK ? q0 * p.H : h0, PACK ? 0 : q0);
       }
       __syncwarp();
       constexpr uint32_t id_qk = tc::idesc_bf16_f32(kRowsT, kHT, false, false);
@@ -346,64 +462,104 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       }
     }
   } else if (warp < 4 + kSoft) {
-    tc::setmaxnreg_inc<96>();
-
     // ------------------------------ softmax ------------------------------
-    const int quarter = warp & 3, hsel = (warp - 4) >> 2;  // TMEM lanes of this warp; heads [32 hsel, 32 hsel + 32)
+    tc::setmaxnreg_dec<64>();
+    const int hsel = (warp - 4) >> 2;  // columns [32 hsel, 32 hsel + 32)
     const int row = quarter * 32 + lane, st = threadIdx.x - 128;
-    const uint32_t lanebase = (uint32_t)(quarter * 32) << 16;
     const float scale_log2 = p.scale * kLog2e;
-    // Heads are taken 16 at a time, to keep the registers of a thread few.
-    float lw = 0.f;  // lane l: head 32 hsel + l's sum over this warp's rows, relative to the running maximum
+    // The rotation by -t of the output channels that this thread will hold in the last two blocks (unsplit queries):
+    // taken now, while the first rows are under way.  Channel d pairs with d ^ 1, the neighbouring lane.
+    float rc0 = 1.f, rs0 = 0.f, rc1 = 1.f, rs1 = 0.f;
+    if (!PACK && splits == 1 && p.rope_dims > 0) {
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        const int d = (kBlocks - 2 + k) * 128 + row - (kC - p.rope_dims);
+        float cs = 1.f, sn = 0.f;
+        if (d >= 0) rope_cos_sin(grp.t, d >> 1, p.rope_dims, p.rope_base, cs, sn);
+        rc0 = rc1;
+        rs0 = rs1;
+        rc1 = cs;
+        rs1 = (d & 1) ? -sn : sn;
+      }
+    }
+    // Columns are taken 16 at a time, to keep the registers of a thread few.
+    float lw = 0.f;  // lane l: column 32 hsel + l's sum over this warp's rows, relative to the running maximum
     unsigned char* prow = base + kOffP + row * 128;
     bool failed = false;
-    for (int i = 0; i < nt; ++i) {
+    int i = 0, g = 0;
+    for (int j = 0; j < grp.n && !failed;) {
+     const Run r = grp.run(p, j, lane);
+     j = r.j1;
+     const int la = max(ga - g, 0), lb = min(gb - g, r.n);
+     g += r.n;
+     // packed: the rows that column 32 hsel + lane sees: entries below ecount; window tokens wlo .. wlo + wcount - 1
+     int ecount = 0, wlo = 0, wcount = 0;
+     if (PACK) {
+       const int jc = (32 * hsel + lane) / p.H;
+       const int tc_ = __shfl_sync(0xffffffffu, grp.t, min(jc, 31)), vc = __shfl_sync(0xffffffffu, grp.vis, min(jc, 31));
+       if (jc >= r.j0 && jc < r.j1) {
+         ecount = vc;
+         wlo = max(0, tc_ - p.n_win + 1);
+         wcount = tc_ - wlo + 1;
+       }
+     }
+     for (int lt = la; lt < lb; ++lt, ++i) {
       const uint32_t ph = i & 1;
       // (block 0 landed long before S: this wait orders the converters' row flags before their use here)
       failed = !tc::warp_wait(&bars->vfull[0], ph, abort) || !tc::warp_wait(&bars->sfull, ph, abort);
       const bool valid = !failed && ((bars->rowok[i & 3][row >> 3] >> (4 * (row & 7))) & 1u);
-      const float bias = valid ? 0.f : neg_inf();
-      // scores of heads 16 x .. 16 x + 15 of this warp's in units of log2, -inf in rows that take no part
-      auto load_scores = [&](int x, float (&sv)[16]) {
-        uint32_t v[16];
+      const uint32_t vmask = valid ? 0xffffffffu : 0u;
+      // Columns that see this row.  Only tiles with rows that some column of the group does not see look at them.
+      uint32_t sees = 0xffffffffu;
+      const bool masked = PACK && (r.j1 - r.j0 < grp.n || lt >= r.na || (lt + 1) * kRowsT > r.least);
+      if (masked) {
+        const int pos = lt < r.na ? lt * kRowsT + row : r.tok0 + (lt - r.na) * kRowsT + row;
+        sees = 0u;
+#pragma unroll 1
+        for (int c = 0; c < 32; ++c) {
+          const int lo = __shfl_sync(0xffffffffu, lt < r.na ? 0 : wlo, c);
+          const int n = __shfl_sync(0xffffffffu, lt < r.na ? ecount : wcount, c);
+          if ((unsigned int)(pos - lo) < (unsigned int)n) sees |= 1u << c;
+        }
+      }
+      // scores of heads 16 x .. 16 x + 15 of this warp's
+      auto load_scores = [&](int x, uint32_t (&v)[16]) {
         tc::tmem_ld16(tmem + lanebase + kColS + kHpt * hsel + 16 * x, v);
         tc::tmem_ld_wait();
-#pragma unroll
-        for (int h = 0; h < 16; ++h) sv[h] = fmaf(__uint_as_float(v[h]), scale_log2, bias);
       };
-      // ... relative to the running maxima
-      auto subtract_maxima = [&](int x, float (&sv)[16]) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float4 m4 = *reinterpret_cast<const float4*>(bars->mref + kHpt * hsel + 16 * x + 4 * c);
-          sv[4 * c] -= m4.x;
-          sv[4 * c + 1] -= m4.y;
-          sv[4 * c + 2] -= m4.z;
-          sv[4 * c + 3] -= m4.w;
-        }
-      };
-      // P(i) against the running maxima (PV(i-1), the last reader of the buffer, has completed); returns the largest
-      // score relative to its head's maximum
+      // P(i) against the running maxima (PV(i-1), the last reader of the buffer, has completed), zeros in rows that
+      // take no part; returns the largest score (in units of log2) relative to its head's maximum
       auto write_p = [&]() -> float {
         float top = neg_inf();
 #pragma unroll
         for (int x = 0; x < kHpt / 16; ++x) {
+          uint32_t v[16], w[8];
+          load_scores(x, v);
           float sv[16];
-          load_scores(x, sv);
-          subtract_maxima(x, sv);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float4 m4 = *reinterpret_cast<const float4*>(bars->nref + kHpt * hsel + 16 * x + 4 * c);
+            sv[4 * c] = fmaf(__uint_as_float(v[4 * c]), scale_log2, m4.x);
+            sv[4 * c + 1] = fmaf(__uint_as_float(v[4 * c + 1]), scale_log2, m4.y);
+            sv[4 * c + 2] = fmaf(__uint_as_float(v[4 * c + 2]), scale_log2, m4.z);
+            sv[4 * c + 3] = fmaf(__uint_as_float(v[4 * c + 3]), scale_log2, m4.w);
+          }
+          if (PACK && masked) {
+#pragma unroll
+            for (int h = 0; h < 16; ++h) sv[h] = (sees >> (16 * x + h)) & 1u ? sv[h] : neg_inf();
+          }
 #pragma unroll
           for (int h = 0; h < 16; h += 2) top = fmaxf(top, fmaxf(sv[h], sv[h + 1]));
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            const int c = (kHpt / 8) * hsel + 2 * x + cc;  // 16-byte unit of the row: heads 8c .. 8c+7
-            uint32_t w[4];
+          for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(fast_exp2(sv[2 * k]), fast_exp2(sv[2 * k + 1])) & vmask;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = pack_bf16x2(fast_exp2(sv[8 * cc + 2 * j]), fast_exp2(sv[8 * cc + 2 * j + 1]));
-            *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int cc = 0; cc < 2; ++cc) {
+            const int c = (kHpt / 8) * hsel + 2 * x + cc;  // 16-byte unit of the row: columns 8c .. 8c+7
+            *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
+                make_uint4(w[4 * cc], w[4 * cc + 1], w[4 * cc + 2], w[4 * cc + 3]);
           }
         }
-        return top;
+        return valid ? top : neg_inf();
       };
       if (!failed) tc::fence_after_sync();
       const float top = i == 0 ? INFINITY : write_p();  // (the first tile sets the maxima in any case)
@@ -413,18 +569,24 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
         if (tc::named_bar_or(1, 32 * kSoft, failed || *abort)) { failed = true; break; }
 #pragma unroll 1
         for (int x = 0; x < kHpt / 16; ++x) {
-          float sv[16];
-          load_scores(x, sv);
-          const float m = warp_reduce16<true>(sv, lane);
+          uint32_t v[16];
+          load_scores(x, v);
+          const uint32_t ok = (sees & vmask) >> (16 * x);
+          float m = 0.f;
+#pragma unroll
+          for (int h = 0; h < 16; ++h) {
+            const float y = warp_max((ok >> h) & 1u ? __uint_as_float(v[h]) * scale_log2 : neg_inf());
+            if (lane == h) m = y;
+          }
           if (lane < 16) bars->red[quarter][kHpt * hsel + 16 * x + lane] = m;
         }
         tc::named_bar(1, 32 * kSoft);
         if (st < kHT) {
           const float mt = fmaxf(fmaxf(bars->red[0][st], bars->red[1][st]), fmaxf(bars->red[2][st], bars->red[3][st]));
-          const float mo = bars->mref[st];
+          const float mo = -bars->nref[st];
           const bool grow = mt > mo + kRescaleLog2;
           bars->alpha[st] = grow ? fast_exp2(mo - mt) : 1.f;
-          if (grow) bars->mref[st] = mt;
+          if (grow) bars->nref[st] = -mt;
         }
         tc::named_bar(1, 32 * kSoft);
         lw *= bars->alpha[kHpt * hsel + lane];
@@ -462,83 +624,35 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
 #pragma unroll
           for (int h = 0; h < 8; ++h) sv[8 * cc + h] = f[h];
         }
-        const float t = warp_reduce16<false>(sv, lane);
+        const float t = warp_sum16(sv, lane);
         if ((lane >> 4) == x) lw += t;
       }
+     }
     }
-    // ---- epilogue: O^T (channels x heads) and l ----
+    // ---- epilogue: O^T (channels x columns) and the row sums ----
     bars->red[quarter][kHpt * hsel + lane] = lw;
-    bool ok = !failed;
-    if (ok && nt > 0) ok = tc::warp_wait(&bars->odone, (nt - 1) & 1, abort);
-    ok = !tc::named_bar_or(1, 32 * kSoft, !ok || *abort);
-    if (ok) {
-      tc::fence_after_sync();
-      const int dl = quarter * 32 + lane;  // channel within its block
-      // reciprocal row sums (unsplit queries), once per head; a sink logit joins the denominator here (base-2, against
-      // the head's running maximum), for split queries in the combine
-      if (splits == 1) {
-        if (st < kHT) {
-          float l = (bars->red[0][st] + bars->red[1][st]) + (bars->red[2][st] + bars->red[3][st]);
-          if (p.sink != nullptr && h0 + st < p.H && l > 0.f) l += fast_exp2(p.sink[h0 + st] * kLog2e - bars->mref[st]);
-          bars->alpha[st] = l > 0.f ? __fdividef(1.f, l) : 0.f;
-        }
-        tc::named_bar(1, 32 * kSoft);
-      }
-      const int rope0 = kC - p.rope_dims;
-      bf16* stage = reinterpret_cast<bf16*>(base + kOffKv);  // the last PV has read the tile
-      const long long part0 = ((long long)q * splits + sp) * p.H + h0;
-#pragma unroll 1
-      for (int part = 0; part < kBlocks * (kHpt / 16); ++part) {
-        const int b = part >> 1, hh = kHpt * hsel + 16 * (part & 1);
-        uint32_t v[16];
-        if (nt > 0) {
-          tc::tmem_ld16(tmem + lanebase + kColO + b * kHT + hh, v);
-          tc::tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int h = 0; h < 16; ++h) v[h] = 0u;
-        }
-        const int d = b * 128 + dl;
-        if (splits > 1) {
-          float* wo = ws_o + (part0 + hh) * kC + d;
-#pragma unroll
-          for (int h = 0; h < 16; ++h)
-            if (h0 + hh + h < p.H) wo[h * kC] = __uint_as_float(v[h]);
-          continue;
-        }
-        // output rotation by -t: channel d pairs with d ^ 1, the neighbouring lane; whole warps take the branch
-        const bool rot = p.rope_dims > 0 && b * 128 + quarter * 32 + 31 >= rope0;
-        float rc = 1.f, rs = 0.f;
-        if (rot && d >= rope0) {
-          float sn;
-          rope_cos_sin(r.t, (d - rope0) >> 1, p.rope_dims, p.rope_base, rc, sn);
-          rs = (d & 1) ? -sn : sn;
-        }
-#pragma unroll
-        for (int h = 0; h < 16; ++h) {
-          const float inv = bars->alpha[hh + h];
-          float o = inv != 0.f ? __uint_as_float(v[h]) * inv : 0.f;
-          if (rot) o = fmaf(o, rc, __shfl_xor_sync(0xffffffffu, o, 1) * rs);
-          stage[(hh + h) * kOutLd + d] = __float2bfloat16_rn(o);
-        }
-      }
-      if (splits == 1) {
-        tc::named_bar(1, 32 * kSoft);
-        bf16* out = p.out + ((long long)q * p.H + h0) * kC;
-        const int nh = min(kHT, p.H - h0);
-        for (int u = st; u < nh * (kC / 8); u += 32 * kSoft) {
-          const int h = u / (kC / 8), x = u % (kC / 8);
-          *reinterpret_cast<uint4*>(out + h * kC + x * 8) = *reinterpret_cast<const uint4*>(stage + h * kOutLd + x * 8);
-        }
+    tc::named_bar(1, 32 * kSoft);
+    if (!failed && st < kHT) {
+      float l = (bars->red[0][st] + bars->red[1][st]) + (bars->red[2][st] + bars->red[3][st]);
+      if (PACK || splits > 1) {
+        const int to = column_row(st);
+        if (to >= 0) ws_ml[to] = make_float2(l > 0.f ? -bars->nref[st] : neg_inf(), l);
       } else {
-        if (st < kHT && h0 + st < p.H) {
-          const float l = (bars->red[0][st] + bars->red[1][st]) + (bars->red[2][st] + bars->red[3][st]);
-          ws_ml[part0 + st] = make_float2(l > 0.f ? bars->mref[st] : neg_inf(), l);
-        }
+        // a sink logit joins the denominator here (base-2, against the running maximum), for partial states in the
+        // combine
+        if (p.sink != nullptr && h0 + st < p.H && l > 0.f) l += fast_exp2(p.sink[h0 + st] * kLog2e + bars->nref[st]);
+        bars->alpha[st] = l > 0.f ? __fdividef(1.f, l) : 0.f;
       }
+    }
+    if (all_done(!failed)) {
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k)
+        store_part(2 + (k >> 1), 2 * hsel + (k & 1), k < 2 ? rc0 : rc1, k < 2 ? rs0 : rs1);
+      copy_out();
     }
   } else {
     // ------------------------------ converters ------------------------------
+    tc::setmaxnreg_inc<88>();
     const int cw = warp - 4 - kSoft;
     const int row = 8 * cw + (lane >> 2), sub = lane & 3;    // row of the tile; group 4b + sub of block b
     const int n_groups = (kC - p.kv.rope_dims) / kFp4Group;  // groups held in 4 bits
@@ -551,11 +665,18 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     // store phase (two rows, four groups) hit eight different units.
     const uint32_t unit0 = 4 * (sub & 1) + 2 * chunk;
     unsigned char* kv = base + kOffKv + row * 128;
-    // Entry of this thread's row of tile i, and its cache row (-1: none).
-    auto entry_of = [&](int i) -> int {
-      if (i >= tiles.na || row >= tiles.rows(i)) return -1;
-      const int u = tiles.first(i) + row;
-      return r.idx ? r.idx[u] : u;
+    bool okw = true;
+    int i = 0, g = 0;
+    for (int j = 0; j < grp.n && okw;) {
+    const Run r = grp.run(p, j, lane);
+    j = r.j1;
+    const int la = max(ga - g, 0), lb = min(gb - g, r.n), le = min(lb, r.na);
+    g += r.n;
+    // Entry of this thread's row of the run's tile lt (-1: none), among those of this CTA.
+    auto entry_of = [&](int lt) -> int {
+      const int u = lt * kRowsT + row;
+      if (lt >= le || u >= r.entries) return -1;
+      return grp.idx ? grp.idx[u] : u;
     };
     // The block that entry e lies in (paged), loaded but not looked at yet, and its cache row from it.
     auto block_of = [&](int e) -> int {
@@ -563,9 +684,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       const unsigned int j = div_by(e, p.rpb);
       return j < p.kv.bt_stride ? p.kv.bt[r.req * p.kv.bt_stride + j] : -1;
     };
-    auto resolve = [&](int i, int e, int blk) -> int {
-      if (p.check && sub == 0 && r.idx && i < tiles.na && row < tiles.rows(i)) {
-        const unsigned int k = entry_check(e, r.t, p.rate, p.N);
+    auto resolve = [&](int lt, int e, int blk) -> int {
+      if (p.check && sub == 0 && grp.idx && lt < le && lt * kRowsT + row < r.entries) {
+        const unsigned int k = entry_check(e, grp.t, p.rate, p.N);
         if (k) atomicOr(&g_mqa_fp4_error, k << 1);
       }
       if (e < 0 || e >= p.N) return -1;
@@ -601,11 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     };
     // An entry's index, its block and its row are dependent loads, each given a tile's time: x is the cache row of the
     // tile being converted, e1 and b1 entry and block of the next one, e2 the entry of the one after.
-    const int e0 = entry_of(0);
-    int e1 = entry_of(1), e2 = entry_of(2);
-    int x = resolve(0, e0, block_of(e0));
+    const int e0 = entry_of(la);
+    int e1 = entry_of(la + 1), e2 = entry_of(la + 2);
+    int x = resolve(la, e0, block_of(e0));
     int b1 = block_of(e1);
-    if (rope64 && tiles.na > 0) copy_rope(0, x);
+    if (rope64 && la < le) copy_rope(i, x);  // (PV of tile i-2 has released this buffer)
     // Widen this thread's group of block b (one that is not held in 4 bits: its codes are zeros).
     auto widen = [&](int b, const uint4& v, uint32_t scale_word, uint4 (&o)[4]) {
       e2m1x32_to_bf16(v, (int)((scale_word >> (8 * sub)) & 255u) - 127, o);
@@ -629,39 +750,38 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->vfull[b]);
     };
-    bool okw = true;
-    int i = 0;
-    for (; okw && i < tiles.na; ++i) {
+    int lt = la;
+    for (; okw && lt < le; ++lt, ++i) {
       const uint32_t ph = i & 1;
       const uint32_t mask = __ballot_sync(0xffffffffu, x >= 0);
       if (lane == 0) bars->rowok[i & 3][cw] = mask;
-      uint4 oa[4], ob[4];
+      uint4 oa[4], ob[4], oc[4];
       const uint4 sc = fetch_scales(x);
       const uint4 v0 = fetch(x, 0), v1 = fetch(x, 1), v2 = fetch(x, 2), v3 = fetch(x, 3);
       widen(0, v0, sc.x, oa);
       widen(1, v1, sc.y, ob);
+      widen(2, v2, sc.z, oc);
       if (!(okw = tc::warp_wait(&bars->vempty[0], ph ^ 1, abort))) break;
       put(i, 0, oa);
-      widen(2, v2, sc.z, oa);
-      if (!(okw = tc::warp_wait(&bars->vempty[1], ph ^ 1, abort))) break;
-      put(i, 1, ob);
-      widen(3, v3, sc.w, ob);
+      widen(3, v3, sc.w, oa);
       if (!(okw = tc::warp_wait(&bars->vempty[kBlocks - 1], ph ^ 1, abort))) break;
-      put(i, 2, oa);
-      put(i, 3, ob);
+      put(i, 1, ob);
+      put(i, 2, oc);
+      put(i, 3, oa);
       // PV of tile i-1 has released its buffer of the last chunk: it takes tile i+1's
-      x = resolve(i + 1, e1, b1);
-      if (rope64 && i + 1 < tiles.na) copy_rope(i + 1, x);
+      x = resolve(lt + 1, e1, b1);
+      if (rope64 && lt + 1 < le) copy_rope(i + 1, x);
       e1 = e2;
       b1 = block_of(e1);
-      e2 = entry_of(i + 3);
+      e2 = entry_of(lt + 3);
     }
-    for (; okw && i < nt; ++i) {  // window rows
+    for (; okw && lt < lb; ++lt, ++i) {  // window rows
       const uint32_t ph = i & 1;
-      const bool valid = row < tiles.rows(i);
+      const int w = (lt - r.na) * kRowsT + row;
+      const bool valid = w < r.window;
       const uint32_t mask = __ballot_sync(0xffffffffu, valid);
       if (lane == 0) bars->rowok[i & 3][cw] = mask;
-      const bf16* src = valid ? window_row(p, r, tiles.first(i) + row) : p.win;
+      const bf16* src = valid ? p.win + r.req * p.win_seq_stride + (long long)((r.tok0 + w) % p.win_rows) * kC : p.win;
 #pragma unroll 1
       for (int b = 0; b < kBlocks; ++b) {
         if (!tc::warp_wait(&bars->vempty[b], ph ^ 1, abort)) { okw = false; break; }
@@ -680,7 +800,13 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       __syncwarp();
       if (okw && lane == 0) tc::mbar_arrive(&bars->vfull[kBlocks - 1]);
     }
+    }
     tc::cp_async_wait<0>();
+    if (all_done(okw)) {
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) store_part(k, cw >> 2, 1.f, 0.f);
+      copy_out();
+    }
   }
 
   tc::fence_before_sync();
@@ -694,16 +820,22 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
 extern cudaError_t make_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                                   const uint64_t* strides_bytes, uint32_t box_rows);
 
+// Queries that share a CTA's 64 columns (1: not packed).
+static int packed_queries(const MqaFp4Problem& p) {
+  return p.kv.c == kC && p.q_req && !p.idx && p.H <= kHT / 2 && p.Tq > 1 ? min(32, kHT / p.H) : 1;
+}
+
 // Splits per query: fewest tiles on the critical path over whole waves of CTAs (one per SM), a CTA's set-up and
 // epilogue counted as three quarters of a tile each (tcgen05); about eight CTAs per SM (CUDA cores).
 MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms) {
   MqaPlan pl;
   const int entries = p.idx ? p.n_idx : p.N, window = p.win ? p.n_win : 0;
   pl.max_rows = max(1, entries + window);
+  const size_t state = (size_t)p.Tq * p.H * ((size_t)p.kv.c * sizeof(float) + sizeof(float2));
   if (p.kv.c == kC) {
-    const int groups = (p.H + kHT - 1) / kHT;
-    const int tiles = max(1, (entries + kRowsT - 1) / kRowsT + (window + kRowsT - 1) / kRowsT);
-    const long long ctas1 = (long long)max(1, p.Tq) * groups;
+    const int pack = packed_queries(p);
+    const int tiles = max(1, (entries + kRowsT - 1) / kRowsT + (window + pack - 1 + kRowsT - 1) / kRowsT);
+    const long long ctas1 = (long long)((max(1, p.Tq) + pack - 1) / pack) * ((p.H + kHT - 1) / kHT);
     const int smax = (int)min((long long)min(tiles, 1024), max(1ll, 2ll * num_sms / ctas1));
     int best = 1;
     long long best_cost = -1;
@@ -713,10 +845,9 @@ MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms) {
       const long long cost = waves * (tpc * 4 + 6) + (eff > 1 ? 4 : 0);
       if (best_cost < 0 || cost < best_cost) { best_cost = cost; best = eff; }
     }
-    const int tpc = (tiles + best - 1) / best;
     pl.splits = best;
-    pl.rows_per_split = tpc * kRowsT;
-    pl.ws_bytes = best > 1 ? (size_t)p.Tq * best * p.H * (kC * sizeof(float) + sizeof(float2)) : 0;
+    pl.rows_per_split = 0;  // (tiles are dealt out on the device)
+    pl.ws_bytes = best > 1 || pack > 1 ? state * best : 0;
     return pl;
   }
   const int groups = (p.H + kSH - 1) / kSH;
@@ -724,8 +855,26 @@ MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms) {
   splits = min(min(splits, 64), (pl.max_rows + kSRows - 1) / kSRows);
   pl.rows_per_split = ((pl.max_rows + splits - 1) / splits + kSRows - 1) / kSRows * kSRows;
   pl.splits = (pl.max_rows + pl.rows_per_split - 1) / pl.rows_per_split;
-  pl.ws_bytes = (size_t)p.Tq * pl.splits * p.H * ((size_t)p.kv.c * sizeof(float) + sizeof(float2));
+  pl.ws_bytes = state * pl.splits;
   return pl;
+}
+
+template <bool PACK>
+static cudaError_t launch_tc(const MqaFp4Problem& p, int pack, int splits, float* ws_o, float2* ws_ml,
+                             cudaStream_t stream) {
+  // rows of the queries: the heads of one query, those past n_heads read as zeros; packed, the heads of all queries
+  CUtensorMap tm_q;
+  const uint64_t rows = PACK ? (uint64_t)p.Tq * p.H : (uint64_t)p.H;
+  const uint64_t qd[3] = {(uint64_t)kC, rows, PACK ? 1ull : (uint64_t)p.Tq};
+  const uint64_t qs[2] = {(uint64_t)kC * 2, rows * kC * 2};
+  cudaError_t e = make_tmap_bf16(&tm_q, p.q, 3, qd, qs, kHT);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute((const void*)mqa_fp4_tc_kernel<PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const long long ctas = (long long)((p.Tq + pack - 1) / pack) * (PACK ? 1 : (p.H + kHT - 1) / kHT) * splits;
+  mqa_fp4_tc_kernel<PACK><<<(unsigned)ctas, kThreads, kSmemBytes, stream>>>(tm_q, p, pack, splits, ws_o, ws_ml);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_mqa_fp4(const MqaFp4Problem& problem, const MqaPlan& pl, void* ws, cudaStream_t stream) {
@@ -735,26 +884,19 @@ cudaError_t launch_mqa_fp4(const MqaFp4Problem& problem, const MqaPlan& pl, void
   float* ws_o = reinterpret_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)p.Tq * pl.splits * p.H * p.kv.c);
   cudaError_t e;
+  const int pack = packed_queries(p);
   if (p.kv.c == kC) {
-    CUtensorMap tm_q;
-    const uint64_t qd[3] = {(uint64_t)kC, (uint64_t)p.H, (uint64_t)p.Tq};
-    const uint64_t qs[2] = {(uint64_t)kC * 2, (uint64_t)p.H * kC * 2};
-    e = make_tmap_bf16(&tm_q, p.q, 3, qd, qs, kHT);  // heads past n_heads read as zeros
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute((const void*)mqa_fp4_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmemBytes);
-    if (e != cudaSuccess) return e;
-    const int groups = (p.H + kHT - 1) / kHT;
-    mqa_fp4_tc_kernel<<<(unsigned)(p.Tq * groups * pl.splits), kThreads, kSmemBytes, stream>>>(
-        tm_q, p, pl.splits, pl.rows_per_split, ws_o, ws_ml);
+    e = pack > 1 ? launch_tc<true>(p, pack, pl.splits, ws_o, ws_ml, stream)
+                 : launch_tc<false>(p, pack, pl.splits, ws_o, ws_ml, stream);
   } else {
     const int groups = (p.H + kSH - 1) / kSH;
     mqa_fp4_simple_kernel<<<(unsigned)(p.Tq * groups * pl.splits), kSThreads, 0, stream>>>(
         p, pl.splits, pl.rows_per_split, ws_o, ws_ml);
+    e = cudaGetLastError();
   }
+  if (e != cudaSuccess) return e;
   ++g_launch_counter;
-  e = cudaGetLastError();
-  if (e != cudaSuccess || (p.kv.c == kC && pl.splits == 1)) return e;
+  if (p.kv.c == kC && pack == 1 && pl.splits == 1) return cudaSuccess;
   return launch_mqa_combine(ws_o, ws_ml, p.Tq, pl.splits, p.H, p.kv.c, p.out, p.sink, p.q_pos, p.rope_dims, p.rope_base,
                             stream, true);
 }

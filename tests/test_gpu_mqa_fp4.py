@@ -173,6 +173,36 @@ def test_several_queries_a_request(nq, H):
     s.check(s.call(pos, q_req=req), pos, q_req=req)
 
 
+@pytest.mark.parametrize("H,nq", [(1, 70), (2, 33), (5, 29), (7, 13), (16, 21), (24, 9), (32, 5)])
+@pytest.mark.parametrize("N", [90, 700])
+def test_queries_that_share_columns(H, nq, N):
+    """Few heads: the columns of one CTA belong to several queries, whose requests and positions change inside it."""
+    s = Setup(H=H, B=3, N=N, rpb=16, nq=nq, W=700, seed=H)
+    rng = np.random.default_rng(H)
+    req = np.repeat([2, 0, 1], nq)
+    pos = np.concatenate([4 * N - 3 - nq + np.arange(nq), 40 + np.arange(nq), 200 + np.arange(nq)])
+    z = rng.normal(size=H)
+    s.check(s.call(pos, q_req=req, rotate=True, sink=z), pos, q_req=req, rotate=True, sink=z)
+    # any order of requests, positions far apart and equal, padding queries in between
+    req = rng.integers(0, 3, 3 * nq)
+    req[nq // 2: nq // 2 + 6] = 1
+    pos = rng.integers(0, 4 * N + 50, 3 * nq)
+    pos[nq // 2: nq // 2 + 6] = [300, 303, 299, 299, 304, 309]
+    pos[5], req[8] = -1, 3
+    s.check(s.call(pos, q_req=req), pos, q_req=req)
+    s.win = None
+    s.check(s.call(pos, q_req=req, sink=z), pos, q_req=req, sink=z)
+
+
+def test_one_query_a_request_named():
+    """q_req names the same requests as its absence, in another order, for one query each."""
+    s = Setup(H=8, B=5, N=300, rpb=0, seed=4)
+    pos = np.array([1199, 700, 3, 1100, 1000])
+    s.check(s.call(pos, q_req=np.arange(5)), pos, q_req=np.arange(5))
+    req = np.array([3, 1, 4, 0, 2])
+    s.check(s.call(pos, q_req=req), pos, q_req=req)
+
+
 def test_many_queries_unsplit():
     """More queries than the machine has room for: one CTA walks all of a query's rows."""
     s = Setup(H=64, B=1, N=600, nq=400, seed=3)
