@@ -523,6 +523,13 @@ typedef struct {
    * newest HCA entry is written in FP8 form to row hca_N-1.  Not with paged caches. */
   const hca_kv_fp8* csa_kv8;
   const hca_kv_fp8* hca_kv8;
+  /* FP4 caches (see kv_cache_append; host pointers to descriptors, flat or paged in
+   * their own arrangement), or NULL: the layer's entries are read from them (csa_kv /
+   * hca_kv, csa_kv8 / hca_kv8 are not given) as in sparse_mqa_attend_fp4, whether the
+   * indexer's keys are flat, paged (block_table) or MXFP4.  With hca_block_cand the
+   * newest HCA entry is appended as entry hca_N-1. */
+  const hca_kv_cache* csa_kv4;
+  const hca_kv_cache* hca_kv4;
 } hca_decode_args;
 
 int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* args, void* ws,

@@ -57,7 +57,7 @@ class DecodeArgs(ctypes.Structure):
                 ("csa_norm", c_void_p), ("hca_norm", c_void_p),
                 ("csa_k_codes", c_void_p), ("csa_k_scales", c_void_p), ("csa_k4_stride", c_ll),
                 ("block_table", c_void_p), ("bt_stride", c_ll), ("n_pool_blocks", c_int),
-                ("csa_kv8", c_void_p), ("hca_kv8", c_void_p)]
+                ("csa_kv8", c_void_p), ("hca_kv8", c_void_p), ("csa_kv4", c_void_p), ("hca_kv4", c_void_p)]
 
 
 class KvFp8(ctypes.Structure):
@@ -529,12 +529,14 @@ def _events_array(events):
 
 def make_decode_args(B, q_pos, csa=None, hca=None, csa_topk_idx=None, csa_out=None, hca_out=None, events=None,
                      csa_sink=None, hca_sink=None, csa_norm=None, hca_norm=None, csa_k4=None, csa_kv8=None,
-                     hca_kv8=None):
+                     hca_kv8=None, csa_kv4=None, hca_kv4=None):
     """Build DecodeArgs from dicts of tensors (see workloads.csa_decode_inputs /
     hca_decode_inputs); csa_sink / hca_sink: optional [H] float32 sink logits;
     csa_norm / hca_norm: optional [2, c] float32 Q/KV normalisation weights;
     csa_k4: optional (codes uint8 [B, N_alloc, 64], scales uint8 [B, N_alloc, 4]),
-    the MXFP4 indexer keys of the FP4 indexer variant (see mxfp4_quantize).
+    the MXFP4 indexer keys of the FP4 indexer variant (see mxfp4_quantize);
+    csa_kv4 / hca_kv4: optional KvCache in FP4 form that holds the layer's entries
+    (their number per request is then csa["N"] / hca["N"]).
     Returns (args, keepalive)."""
     a = DecodeArgs()
     # FP8 caches: (codes, scales, rope) triples from kv_fp8_quantize
@@ -544,6 +546,10 @@ def make_decode_args(B, q_pos, csa=None, hca=None, csa_topk_idx=None, csa_out=No
             desc = make_kv_fp8(*t)
             setattr(a, name, ctypes.cast(ctypes.pointer(desc), c_void_p))
             d8.append(desc)
+    for name, k in (("csa_kv4", csa_kv4), ("hca_kv4", hca_kv4)):
+        if k is not None:
+            setattr(a, name, ctypes.addressof(k.desc))
+            d8.append(k)
     if csa_k4 is not None:
         codes, scales = csa_k4
         a.csa_k_codes = _ptr(codes, torch.uint8, "csa_k4 codes")
@@ -565,7 +571,7 @@ def make_decode_args(B, q_pos, csa=None, hca=None, csa_topk_idx=None, csa_out=No
         E = csa.get("E")  # (not read with an FP8 cache)
         a.csa_kv = _ptr(E, BF16, "csa.E")
         a.csa_k_idx = _ptr(csa.get("K_I"), BF16, "csa.K_I")  # (not read by the FP4 variant)
-        a.csa_N = E.shape[1] if E is not None else csa_kv8[0].shape[1]
+        a.csa_N = E.shape[1] if E is not None else csa_kv8[0].shape[1] if csa_kv8 is not None else csa["N"]
         a.csa_kv_stride = E.stride(0) if E is not None else 0
         a.csa_k_stride = csa["K_I"].stride(0) if csa.get("K_I") is not None else 0
         a.csa_win = _ptr(csa["win"], BF16, "csa.win")
@@ -576,7 +582,7 @@ def make_decode_args(B, q_pos, csa=None, hca=None, csa_topk_idx=None, csa_out=No
         a.hca_q = _ptr(hca["q"], BF16, "hca.q")
         Eh = hca.get("E_h")  # (not read with an FP8 cache)
         a.hca_kv = _ptr(Eh, BF16, "hca.E_h")
-        a.hca_N = Eh.shape[1] if Eh is not None else hca_kv8[0].shape[1]
+        a.hca_N = Eh.shape[1] if Eh is not None else hca_kv8[0].shape[1] if hca_kv8 is not None else hca["N"]
         a.hca_kv_stride = Eh.stride(0) if Eh is not None else 0
         if hca.get("block_cand") is not None:
             a.hca_block_cand = _ptr(hca["block_cand"], BF16, "hca.block_cand")

@@ -685,6 +685,107 @@ static int check_kv8(const hca_layer_cfg* cfg, const hca_kv_fp8* d, const char* 
   return HCA_OK;
 }
 
+// ---- KV caches in one descriptor, FP4 entries -----------------------------------------
+static int check_cache(const hca_kv_cache* k, const char* who) {
+  CHECK(k != nullptr, HCA_ERR_INVALID_ARG, "%s: cache null", who);
+  CHECK(k->form >= HCA_KV_BF16 && k->form <= HCA_KV_FP4, HCA_ERR_INVALID_ARG, "%s: cache form %d", who, k->form);
+  CHECK(k->c > 0 && k->rope_dims >= 0 && k->rope_dims <= k->c, HCA_ERR_INVALID_ARG, "%s: cache c=%d rope_dims=%d", who,
+        k->c, k->rope_dims);
+  CHECK(k->c % 8 == 0 && k->c <= 512 && k->rope_dims % 8 == 0 && k->rope_dims <= 256, HCA_ERR_UNSUPPORTED,
+        "%s: cache c=%d rope_dims=%d (multiples of 8, at most 512 and 256)", who, k->c, k->rope_dims);
+  const int n = k->c - k->rope_dims;
+  CHECK_PTR(k->codes, who);
+  if (k->form == HCA_KV_BF16) {
+    CHECK(k->ld_codes >= k->c && k->ld_codes % 8 == 0, HCA_ERR_INVALID_ARG, "%s: cache ld_codes %lld", who, k->ld_codes);
+  } else {
+    const int group = k->form == HCA_KV_FP8 ? 64 : 32;
+    CHECK(n > 0 && n % group == 0, HCA_ERR_UNSUPPORTED, "%s: cache c - rope_dims = %d must be a positive multiple of %d",
+          who, n, group);
+    CHECK(k->ld_codes >= (k->form == HCA_KV_FP8 ? n : n / 2) && k->ld_codes % 16 == 0 && k->ld_scales >= n / group,
+          HCA_ERR_INVALID_ARG, "%s: cache row strides (codes %lld, scales %lld)", who, k->ld_codes, k->ld_scales);
+    CHECK(k->scales != nullptr && (k->form == HCA_KV_FP4 || (reinterpret_cast<uintptr_t>(k->scales) & 3u) == 0),
+          HCA_ERR_INVALID_ARG, "%s: cache scales null or misaligned", who);
+    if (k->rope_dims) {
+      CHECK_PTR(k->rope, who);
+      CHECK(k->ld_rope >= k->rope_dims && k->ld_rope % 8 == 0, HCA_ERR_INVALID_ARG, "%s: cache ld_rope %lld", who,
+            k->ld_rope);
+    }
+  }
+  CHECK(k->n_rows >= 0 && k->n_req >= 0, HCA_ERR_INVALID_ARG, "%s: cache n_rows=%lld n_req=%d", who, k->n_rows,
+        k->n_req);
+  if (k->block_table) {
+    CHECK((reinterpret_cast<uintptr_t>(k->block_table) & 3u) == 0 && k->bt_stride >= 1 && k->rows_per_block >= 1,
+          HCA_ERR_INVALID_ARG, "%s: cache block_table misaligned, bt_stride=%lld or rows_per_block=%d", who,
+          k->bt_stride, k->rows_per_block);
+    CHECK(!k->ring, HCA_ERR_UNSUPPORTED, "%s: a paged cache is not a ring", who);
+  } else {
+    CHECK(k->seq_rows >= 1, HCA_ERR_INVALID_ARG, "%s: cache seq_rows=%lld", who, k->seq_rows);
+    CHECK(k->n_req == 0 || k->n_rows / k->n_req >= k->seq_rows, HCA_ERR_INVALID_ARG,
+          "%s: cache of %lld rows for %d requests of %lld", who, k->n_rows, k->n_req, k->seq_rows);
+  }
+  return HCA_OK;
+}
+
+static KvCache kv_cache_of(const hca_kv_cache* d) {
+  KvCache k;
+  k.form = d->form;
+  k.c = d->c;
+  k.rope_dims = d->rope_dims;
+  k.codes = d->codes;
+  k.scales = d->scales;
+  k.rope = reinterpret_cast<bf16*>(d->rope);
+  k.ld_codes = d->ld_codes;
+  k.ld_scales = d->ld_scales;
+  k.ld_rope = d->ld_rope;
+  k.n_rows = d->n_rows;
+  k.seq_rows = d->block_table ? 0 : d->seq_rows;
+  k.ring = d->ring != 0;
+  k.bt = d->block_table;
+  k.bt_stride = d->bt_stride;
+  k.rpb = d->block_table ? d->rows_per_block : 1;
+  k.n_req = d->n_req;
+  return k;
+}
+
+constexpr int kMaxFp4Queries = 1 << 20;
+// The layer fields that the attention over FP4 entries reads.
+static int check_fp4_cfg(const hca_layer_cfg* cfg, const char* who) {
+  CHECK(cfg != nullptr, HCA_ERR_INVALID_ARG, "%s: cfg null", who);
+  CHECK(cfg->c > 0 && cfg->n_heads > 0 && cfg->n_win > 0, HCA_ERR_INVALID_ARG, "%s: cfg sizes must be positive", who);
+  CHECK(cfg->scale > 0.f, HCA_ERR_INVALID_ARG, "%s: cfg scale must be positive", who);
+  CHECK(cfg->c % 32 == 0 && cfg->c <= 512 && cfg->n_heads <= 128, HCA_ERR_UNSUPPORTED,
+        "%s: cfg c=%d n_heads=%d (c a multiple of 32, at most 512; at most 128 heads)", who, cfg->c, cfg->n_heads);
+  return HCA_OK;
+}
+
+static MqaFp4Problem fp4_problem(const hca_layer_cfg* cfg, int Tq, int N, const int32_t* idx, int n_idx,
+                                 const hca_bf16* win) {
+  MqaFp4Problem p = {};
+  p.kv.c = cfg->c;
+  p.N = N;
+  p.idx = idx;
+  p.n_idx = n_idx;
+  p.win = reinterpret_cast<const bf16*>(win);
+  p.n_win = cfg->n_win;
+  p.Tq = Tq;
+  p.H = cfg->n_heads;
+  p.scale = cfg->scale;
+  return p;
+}
+
+// A FP4 cache that an attention reads for n_req requests.
+static int check_kv4(const hca_layer_cfg* cfg, const hca_kv_cache* k, int n_req, const char* who) {
+  const int s = check_cache(k, who);
+  if (s != HCA_OK) return s;
+  CHECK(k->form == HCA_KV_FP4 && !k->ring, HCA_ERR_UNSUPPORTED, "%s: takes a flat or paged cache in FP4 form", who);
+  CHECK(k->c == cfg->c, HCA_ERR_INVALID_ARG, "%s: cache c=%d, cfg c=%d", who, k->c, cfg->c);
+  CHECK(k->n_rows <= 0x7fffffffll, HCA_ERR_UNSUPPORTED, "%s: cache of %lld rows (at most 2^31 - 1)", who, k->n_rows);
+  CHECK(aligned16(k->scales) && k->ld_scales % 16 == 0, HCA_ERR_INVALID_ARG,
+        "%s: cache scales not 16-byte aligned, or ld_scales %lld not a multiple of 16", who, k->ld_scales);
+  CHECK(n_req <= k->n_req, HCA_ERR_INVALID_ARG, "%s: cache of %d requests for %d", who, k->n_req, n_req);
+  return HCA_OK;
+}
+
 // ---- decode ------------------------------------------------------------------
 // When both layers are present, the HCA layer (its block compression and dense
 // attention) runs on a side stream, concurrently with the CSA indexer, on a
@@ -707,6 +808,8 @@ struct DecodeSched {
   // slot indices [B, k]; the HCA layer's visible rows [B, hca_N, c]; the newest HCA
   // entries [B, c] (f32, or bf16 after normalisation) before their FP8 form
   size_t csa8_rows = 0, csa8_idx = 0, hca8_rows = 0, hca8_new = 0;
+  // FP4 caches: the newest HCA entries [B, c] f32 before they are appended
+  size_t hca4_new = 0;
 };
 
 // Geometry of the paged (classical) cache: blocks of lcm(m, m') raw tokens.
@@ -744,6 +847,26 @@ static MqaProblem decode_hca_problem(const hca_layer_cfg* cfg, const hca_decode_
   return p;
 }
 
+// The attention of a layer whose entries are held in FP4 (its cache, queries and outputs set; with Q/KV normalisation
+// the caller puts the normalised queries and window rows in their place).
+static MqaFp4Problem decode_fp4_problem(const hca_layer_cfg* cfg, const hca_decode_args* a, bool csa) {
+  MqaFp4Problem p = fp4_problem(cfg, a->B, csa ? a->csa_N : a->hca_N, csa ? a->csa_topk_idx : nullptr,
+                                csa ? cfg->topk : 0, csa ? a->csa_win : a->hca_win);
+  if (csa && !p.idx) p.idx = reinterpret_cast<const int32_t*>(1);  // (workspace queries)
+  if (!p.win) p.win = reinterpret_cast<const bf16*>(1);
+  p.q = reinterpret_cast<const bf16*>(csa ? a->csa_q : a->hca_q);
+  p.kv = kv_cache_of(csa ? a->csa_kv4 : a->hca_kv4);
+  p.rate = csa ? cfg->m : cfg->m_hca;
+  p.win_seq_stride = csa ? a->csa_win_stride : a->hca_win_stride;
+  p.win_rows = cfg->n_win;
+  p.q_pos = a->q_pos;
+  p.sink = csa ? a->csa_sink : a->hca_sink;
+  p.rope_base = cfg->rope_base;
+  p.out = reinterpret_cast<bf16*>(csa ? a->csa_out : a->hca_out);
+  p.check = debug_checks() ? 1 : 0;
+  return p;
+}
+
 static DecodeSched decode_schedule(const hca_layer_cfg* cfg, const hca_decode_args* a) {
   DecodeSched d;
   d.sms = device_sm_count();
@@ -751,7 +874,8 @@ static DecodeSched decode_schedule(const hca_layer_cfg* cfg, const hca_decode_ar
   MqaProblem pc, ph;
   if (csa) pc = decode_csa_problem(cfg, a);
   if (hcl) ph = decode_hca_problem(cfg, a);
-  d.overlap = csa && hcl && indexer_tc_supported(cfg->n_idx_heads, cfg->d_idx) && mqa_tc_supported(ph) && d.sms >= 16;
+  d.overlap = csa && hcl && indexer_tc_supported(cfg->n_idx_heads, cfg->d_idx) &&
+              (a->hca_kv4 ? cfg->c == 512 : mqa_tc_supported(ph)) && d.sms >= 16;
   if (d.overlap) {
     // Balance the two sides' SM-time: the attention costs about kAttnTileUs per
     // 64 rows on one SM, the indexer streams about kIdxBytesPerSmUs bytes per
@@ -770,14 +894,14 @@ static DecodeSched decode_schedule(const hca_layer_cfg* cfg, const hca_decode_ar
       d.overlap = false;  // too many requests to share the machine this way
     } else {
       d.r_hca = r;
-      d.hca_pl = plan_mqa_sms(ph, r);
+      d.hca_pl = a->hca_kv4 ? plan_mqa_fp4(decode_fp4_problem(cfg, a, false), r) : plan_mqa_sms(ph, r);
     }
   }
   if (!d.overlap && hcl) {
-    d.hca_pl = plan_mqa(ph);
+    d.hca_pl = a->hca_kv4 ? plan_mqa_fp4(decode_fp4_problem(cfg, a, false), d.sms) : plan_mqa(ph);
   }
   if (csa) {
-    d.csa_pl = plan_mqa(pc);
+    d.csa_pl = a->csa_kv4 ? plan_mqa_fp4(decode_fp4_problem(cfg, a, true), d.sms) : plan_mqa(pc);
     d.main_bytes = std::max(plan_indexer(cfg, a->B, a->csa_N, HCA_MODE_DECODE).bytes, d.csa_pl.ws_bytes);
   }
   if (d.overlap) {
@@ -804,7 +928,7 @@ static DecodeSched decode_schedule(const hca_layer_cfg* cfg, const hca_decode_ar
     d.q4 = d.total;
     d.total = d.q4 + round256((size_t)a->B * cfg->n_idx_heads * cfg->d_idx * 2);
   }
-  if (hcl && a->block_table && a->hca_block_cand) {
+  if (hcl && a->block_table && a->hca_block_cand && !a->hca_kv4) {
     d.hca_new = d.total;
     d.total = d.hca_new + round256((size_t)a->B * cfg->c * 2);
   }
@@ -817,6 +941,10 @@ static DecodeSched decode_schedule(const hca_layer_cfg* cfg, const hca_decode_ar
     d.hca8_rows = d.total;
     d.hca8_new = d.hca8_rows + round256((size_t)a->B * a->hca_N * cfg->c * 2);
     d.total = d.hca8_new + round256((size_t)a->B * cfg->c * 4);
+  }
+  if (hcl && a->hca_kv4 && a->hca_block_cand) {
+    d.hca4_new = d.total;
+    d.total = d.hca4_new + round256((size_t)a->B * cfg->c * 4);
   }
   return d;
 }
@@ -852,6 +980,9 @@ static int side_stream(SideStream** out) {
 
 size_t hybrid_attn_decode_workspace(const hca_layer_cfg* cfg, const hca_decode_args* a) {
   if (check_cfg(cfg) != HCA_OK || !a || a->B < 0) return (size_t)-1;
+  if ((a->csa_q && a->csa_kv4 && check_kv4(cfg, a->csa_kv4, a->B, "hybrid_attn_decode_workspace: csa_kv4") != HCA_OK) ||
+      (a->hca_q && a->hca_kv4 && check_kv4(cfg, a->hca_kv4, a->B, "hybrid_attn_decode_workspace: hca_kv4") != HCA_OK))
+    return (size_t)-1;
   if (a->csa_q && indexer_ok(cfg, a->csa_N, HCA_MODE_DECODE) != HCA_OK) return (size_t)-1;
   return decode_ws(cfg, a);
 }
@@ -889,6 +1020,18 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
   }
   if (a->csa_kv8 || a->hca_kv8)
     CHECK(!a->block_table, HCA_ERR_UNSUPPORTED, "hybrid_attn_decode: FP8 caches are not paged");
+  if (a->csa_q && a->csa_kv4) {
+    CHECK(!a->csa_kv8, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: both csa_kv8 and csa_kv4 given");
+    if ((s = check_kv4(cfg, a->csa_kv4, a->B, "hybrid_attn_decode: csa_kv4")) != HCA_OK) return s;
+    CHECK(a->csa_win_stride >= (long long)cfg->n_win * cfg->c || a->B <= 1, HCA_ERR_INVALID_ARG,
+          "hybrid_attn_decode: csa_win_stride %lld", a->csa_win_stride);
+  }
+  if (a->hca_q && a->hca_kv4) {
+    CHECK(!a->hca_kv8, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: both hca_kv8 and hca_kv4 given");
+    if ((s = check_kv4(cfg, a->hca_kv4, a->B, "hybrid_attn_decode: hca_kv4")) != HCA_OK) return s;
+    CHECK(a->hca_win_stride >= (long long)cfg->n_win * cfg->c || a->B <= 1, HCA_ERR_INVALID_ARG,
+          "hybrid_attn_decode: hca_win_stride %lld", a->hca_win_stride);
+  }
   if (a->csa_q && a->csa_kv8 && (s = check_kv8(cfg, a->csa_kv8, "hybrid_attn_decode: csa_kv8")) != HCA_OK) return s;
   if (a->hca_q && a->hca_kv8 && (s = check_kv8(cfg, a->hca_kv8, "hybrid_attn_decode: hca_kv8")) != HCA_OK) return s;
   if (a->csa_q) {
@@ -910,7 +1053,7 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
       CHECK(a->csa_k_stride % 8 == 0, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: csa_k_stride");
     }
     CHECK_PTR(a->csa_topk_idx, "hybrid_attn_decode: csa_topk_idx");
-    s = check_mqa(cfg, a->csa_q, a->csa_kv, a->csa_kv_stride, a->csa_kv8 ? 0 : a->csa_N, a->csa_topk_idx, cfg->topk,
+    s = check_mqa(cfg, a->csa_q, a->csa_kv, a->csa_kv_stride, a->csa_kv8 || a->csa_kv4 ? 0 : a->csa_N, a->csa_topk_idx, cfg->topk,
                   cfg->m,
                   a->csa_win, a->csa_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->csa_out, "hybrid_attn_decode: csa");
     if (s != HCA_OK) return s;
@@ -918,7 +1061,7 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
   }
   if (a->hca_q) {
     CHECK(a->hca_N > 0, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: hca_N=%d", a->hca_N);
-    s = check_mqa(cfg, a->hca_q, a->hca_kv, a->hca_kv_stride, a->hca_kv8 ? 0 : a->hca_N, nullptr, 0, cfg->m_hca,
+    s = check_mqa(cfg, a->hca_q, a->hca_kv, a->hca_kv_stride, a->hca_kv8 || a->hca_kv4 ? 0 : a->hca_N, nullptr, 0, cfg->m_hca,
                   a->hca_win,
                   a->hca_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->hca_out, "hybrid_attn_decode: hca");
     if (s != HCA_OK) return s;
@@ -963,6 +1106,28 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
   char* wsb = reinterpret_cast<char*>(ws);
   const int c = cfg->c, H = cfg->n_heads, nw = cfg->n_win;
   auto run_hca_compress = [&]() -> int {
+    if (a->hca_kv4) {
+      // FP4 cache: the f32 entries, appended (normalised and rotated when asked) as entry hca_N-1 of every request
+      float* ef = reinterpret_cast<float*>(wsb + sched.hca4_new);
+      CUDA_TRY(launch_compress(reinterpret_cast<const bf16*>(a->hca_block_cand), c,
+                               reinterpret_cast<const bf16*>(a->hca_block_logits), c, a->hca_pos_bias, c, a->B,
+                               a->hca_block_stride, cfg->m_hca, c, cfg->m_hca, false, nullptr, c, c, hst, ef),
+               "decode: hca compress");
+      KvAppend ap = {};
+      ap.x = ef;
+      ap.x_f32 = true;
+      ap.ld_x = c;
+      ap.n_rows = ap.B = a->B;
+      ap.first_all = a->hca_N - 1;
+      ap.rate = cfg->m_hca;
+      ap.gamma = a->hca_norm ? a->hca_norm + c : nullptr;
+      ap.eps = cfg->norm_eps;
+      ap.rotate = a->hca_norm != nullptr;
+      ap.rope_base = cfg->rope_base;
+      ap.check = debug_checks() ? 1 : 0;
+      CUDA_TRY(launch_kv_append(ap, kv_cache_of(a->hca_kv4), hst), "decode: hca entry to its FP4 cache");
+      return HCA_OK;
+    }
     if (a->hca_kv8) {
       // FP8 cache: the f32 entries (normalised to bf16 when asked), then their FP8 form in
       // row hca_N-1 of every request
@@ -1031,7 +1196,26 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
     CUDA_TRY(launch_norm_rope(wr, sm), "decode: window normalisation");
     return HCA_OK;
   };
+  // attention over FP4 entries, with the normalised queries and window rows when asked
+  auto run_fp4_attention = [&](bool csa, const float* norm, size_t qn, size_t wn, const MqaPlan& pl, void* aws,
+                               cudaStream_t sm) -> int {
+    MqaFp4Problem p = decode_fp4_problem(cfg, a, csa);
+    if (norm) {
+      p.q = reinterpret_cast<const bf16*>(wsb + qn);
+      p.win = reinterpret_cast<const bf16*>(wsb + wn);
+      p.win_seq_stride = (long long)nw * c;
+      p.rope_dims = cfg->rope_dims;
+    }
+    return cuda_status(launch_mqa_fp4(p, pl, aws, sm), csa ? "decode: csa attention (fp4)" : "decode: hca attention (fp4)");
+  };
   auto run_hca_attention = [&]() -> int {
+    if (a->hca_kv4) {
+      int r = HCA_OK;
+      if (a->hca_norm)
+        r = normalise_layer(a->hca_q, a->hca_win, a->hca_win_stride, a->hca_norm, sched.hca_qn, sched.hca_wn, hst);
+      return r != HCA_OK ? r
+                         : run_fp4_attention(false, a->hca_norm, sched.hca_qn, sched.hca_wn, sched.hca_pl, hws, hst);
+    }
     MqaProblem p = decode_hca_problem(cfg, a);
     if (a->hca_kv8) {
       // the visible rows widened to bf16, read by the attention as its cache
@@ -1080,6 +1264,10 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
     if (s != HCA_OK) return s;
     MqaProblem p = decode_csa_problem(cfg, a);
     if (a->csa_norm) use_normalised(p, cfg, wsb + sched.csa_qn, wsb + sched.csa_wn, true);
+    if (a->csa_kv4) {
+      s = run_fp4_attention(true, a->csa_norm, sched.csa_qn, sched.csa_wn, sched.csa_pl, ws, st);
+      if (s != HCA_OK) return s;
+    }
     if (a->csa_kv8) {
       // the selected rows widened to bf16 in slot order; the attention reads them as a
       // cache of k rows through the slot indices (empty slots stay -1)
@@ -1093,7 +1281,7 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
       p.N = cfg->topk;
       p.idx = slots;
     }
-    CUDA_TRY(launch_mqa(p, sched.csa_pl, ws, st, true), "decode: csa attention");
+    if (!a->csa_kv4) CUDA_TRY(launch_mqa(p, sched.csa_pl, ws, st, true), "decode: csa attention");
     if ((s = mark()) != HCA_OK) return s;
   }
   if (a->hca_q) {
@@ -1340,67 +1528,6 @@ int csa_indexer_topk_fp4(const hca_bf16* q_idx, const float* w_idx, const uint8_
 }
 
 // ---- KV caches: append, gather, attention over FP4 entries -------------------------
-static int check_cache(const hca_kv_cache* k, const char* who) {
-  CHECK(k != nullptr, HCA_ERR_INVALID_ARG, "%s: cache null", who);
-  CHECK(k->form >= HCA_KV_BF16 && k->form <= HCA_KV_FP4, HCA_ERR_INVALID_ARG, "%s: cache form %d", who, k->form);
-  CHECK(k->c > 0 && k->rope_dims >= 0 && k->rope_dims <= k->c, HCA_ERR_INVALID_ARG, "%s: cache c=%d rope_dims=%d", who,
-        k->c, k->rope_dims);
-  CHECK(k->c % 8 == 0 && k->c <= 512 && k->rope_dims % 8 == 0 && k->rope_dims <= 256, HCA_ERR_UNSUPPORTED,
-        "%s: cache c=%d rope_dims=%d (multiples of 8, at most 512 and 256)", who, k->c, k->rope_dims);
-  const int n = k->c - k->rope_dims;
-  CHECK_PTR(k->codes, who);
-  if (k->form == HCA_KV_BF16) {
-    CHECK(k->ld_codes >= k->c && k->ld_codes % 8 == 0, HCA_ERR_INVALID_ARG, "%s: cache ld_codes %lld", who, k->ld_codes);
-  } else {
-    const int group = k->form == HCA_KV_FP8 ? 64 : 32;
-    CHECK(n > 0 && n % group == 0, HCA_ERR_UNSUPPORTED, "%s: cache c - rope_dims = %d must be a positive multiple of %d",
-          who, n, group);
-    CHECK(k->ld_codes >= (k->form == HCA_KV_FP8 ? n : n / 2) && k->ld_codes % 16 == 0 && k->ld_scales >= n / group,
-          HCA_ERR_INVALID_ARG, "%s: cache row strides (codes %lld, scales %lld)", who, k->ld_codes, k->ld_scales);
-    CHECK(k->scales != nullptr && (k->form == HCA_KV_FP4 || (reinterpret_cast<uintptr_t>(k->scales) & 3u) == 0),
-          HCA_ERR_INVALID_ARG, "%s: cache scales null or misaligned", who);
-    if (k->rope_dims) {
-      CHECK_PTR(k->rope, who);
-      CHECK(k->ld_rope >= k->rope_dims && k->ld_rope % 8 == 0, HCA_ERR_INVALID_ARG, "%s: cache ld_rope %lld", who,
-            k->ld_rope);
-    }
-  }
-  CHECK(k->n_rows >= 0 && k->n_req >= 0, HCA_ERR_INVALID_ARG, "%s: cache n_rows=%lld n_req=%d", who, k->n_rows,
-        k->n_req);
-  if (k->block_table) {
-    CHECK((reinterpret_cast<uintptr_t>(k->block_table) & 3u) == 0 && k->bt_stride >= 1 && k->rows_per_block >= 1,
-          HCA_ERR_INVALID_ARG, "%s: cache block_table misaligned, bt_stride=%lld or rows_per_block=%d", who,
-          k->bt_stride, k->rows_per_block);
-    CHECK(!k->ring, HCA_ERR_UNSUPPORTED, "%s: a paged cache is not a ring", who);
-  } else {
-    CHECK(k->seq_rows >= 1, HCA_ERR_INVALID_ARG, "%s: cache seq_rows=%lld", who, k->seq_rows);
-    CHECK(k->n_req == 0 || k->n_rows / k->n_req >= k->seq_rows, HCA_ERR_INVALID_ARG,
-          "%s: cache of %lld rows for %d requests of %lld", who, k->n_rows, k->n_req, k->seq_rows);
-  }
-  return HCA_OK;
-}
-
-static KvCache kv_cache_of(const hca_kv_cache* d) {
-  KvCache k;
-  k.form = d->form;
-  k.c = d->c;
-  k.rope_dims = d->rope_dims;
-  k.codes = d->codes;
-  k.scales = d->scales;
-  k.rope = reinterpret_cast<bf16*>(d->rope);
-  k.ld_codes = d->ld_codes;
-  k.ld_scales = d->ld_scales;
-  k.ld_rope = d->ld_rope;
-  k.n_rows = d->n_rows;
-  k.seq_rows = d->block_table ? 0 : d->seq_rows;
-  k.ring = d->ring != 0;
-  k.bt = d->block_table;
-  k.bt_stride = d->bt_stride;
-  k.rpb = d->block_table ? d->rows_per_block : 1;
-  k.n_req = d->n_req;
-  return k;
-}
-
 int kv_cache_append(const void* x, int x_is_f32, long long ld_x, int n_rows, const int32_t* row_start,
                     const int32_t* first, int B, int rate, const float* gamma, float norm_eps, int rotate,
                     float rope_base, const hca_kv_cache* cache, void* stream) {
@@ -1462,32 +1589,6 @@ int kv_cache_gather(const hca_kv_cache* cache, int B, int n_out, const int32_t* 
   return HCA_OK;
 }
 
-constexpr int kMaxFp4Queries = 1 << 20;
-// The layer fields that the attention over FP4 entries reads.
-static int check_fp4_cfg(const hca_layer_cfg* cfg, const char* who) {
-  CHECK(cfg != nullptr, HCA_ERR_INVALID_ARG, "%s: cfg null", who);
-  CHECK(cfg->c > 0 && cfg->n_heads > 0 && cfg->n_win > 0, HCA_ERR_INVALID_ARG, "%s: cfg sizes must be positive", who);
-  CHECK(cfg->scale > 0.f, HCA_ERR_INVALID_ARG, "%s: cfg scale must be positive", who);
-  CHECK(cfg->c % 32 == 0 && cfg->c <= 512 && cfg->n_heads <= 128, HCA_ERR_UNSUPPORTED,
-        "%s: cfg c=%d n_heads=%d (c a multiple of 32, at most 512; at most 128 heads)", who, cfg->c, cfg->n_heads);
-  return HCA_OK;
-}
-
-static MqaFp4Problem fp4_problem(const hca_layer_cfg* cfg, int Tq, int N, const int32_t* idx, int n_idx,
-                                 const hca_bf16* win) {
-  MqaFp4Problem p = {};
-  p.kv.c = cfg->c;
-  p.N = N;
-  p.idx = idx;
-  p.n_idx = n_idx;
-  p.win = reinterpret_cast<const bf16*>(win);
-  p.n_win = cfg->n_win;
-  p.Tq = Tq;
-  p.H = cfg->n_heads;
-  p.scale = cfg->scale;
-  return p;
-}
-
 // The plan takes a window to be there, so that the size of the workspace does not depend on it.
 static MqaPlan fp4_plan(const hca_layer_cfg* cfg, int Tq, int N, int n_idx, bool q_req) {
   MqaFp4Problem p = fp4_problem(cfg, Tq, N, n_idx ? reinterpret_cast<const int32_t*>(1) : nullptr, n_idx,
@@ -1517,11 +1618,7 @@ int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, c
   const char* who = "sparse_mqa_attend_fp4";
   int s = check_fp4_cfg(cfg, who);
   if (s != HCA_OK) return s;
-  if ((s = check_cache(cache, who)) != HCA_OK) return s;
-  CHECK(cache->form == HCA_KV_FP4 && !cache->ring, HCA_ERR_UNSUPPORTED, "%s: takes a flat or paged cache in FP4 form", who);
-  CHECK(cache->c == cfg->c, HCA_ERR_INVALID_ARG, "%s: cache c=%d, cfg c=%d", who, cache->c, cfg->c);
-  CHECK(aligned16(cache->scales) && cache->ld_scales % 16 == 0, HCA_ERR_INVALID_ARG,
-        "%s: cache scales not 16-byte aligned, or ld_scales %lld not a multiple of 16", who, cache->ld_scales);
+  if ((s = check_kv4(cfg, cache, 0, who)) != HCA_OK) return s;
   CHECK(Tq >= 0 && Tq <= kMaxFp4Queries && N >= 0 && rate >= 1, HCA_ERR_INVALID_ARG, "%s: Tq=%d (at most %d) N=%d rate=%d",
         who, Tq, kMaxFp4Queries, N, rate);
   CHECK(idx ? (n_idx > 0 && n_idx <= 4096) : n_idx == 0, HCA_ERR_INVALID_ARG, "%s: n_idx=%d", who, n_idx);

@@ -106,7 +106,8 @@ struct KvAppend {
   long long ld_x;
   int n_rows;
   const int32_t* row_start;  // [B+1] or nullptr: one row a request
-  const int32_t* first;      // [B]
+  const int32_t* first;      // [B], or nullptr: first_all for every request
+  int first_all;
   int B, rate;
   const float* gamma;        // or nullptr: no normalisation
   float eps;

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv_append_kernel(KvAppend a, Kv
       start = i;
       end = i + 1;
     }
-    const int f = a.first[b];
+    const int f = a.first ? a.first[b] : a.first_all;
     const long long e = (long long)f + (i - start);
     if (f < 0) continue;
     if (k.ring && (long long)end - i > k.seq_rows) continue;  // a later row of this call takes its place

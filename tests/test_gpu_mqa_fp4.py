@@ -29,6 +29,32 @@ def make(c, H, n_win=128, rope=64, m=4):
                                         scale=c ** -0.5, rope_dims=rope, rope_base=BASE, norm_eps=1e-6))
 
 
+def check_query(got, q, rows, scale, sink=None, rotate_by=None, rope=64, what=""):
+    """One query's output [H, c] against the definition, within the bounds derived above."""
+    c = q.shape[1]
+    z = None if sink is None else np.asarray(sink, dtype=np.float64)
+    o = oracle.mqa_attend(q, rows, scale, z)
+    s = scale * (q @ rows.T)
+    m = s.max(1, keepdims=True) if z is None else np.maximum(s.max(1, keepdims=True), z[:, None])
+    p = np.exp(s - m)
+    p /= p.sum(1, keepdims=True) + (0 if z is None else np.exp(z[:, None] - m))
+    mass = p @ np.abs(rows)
+    e_s = 520 * 2.0 ** -24 * scale * (np.abs(q) @ np.abs(rows).T).max(1, keepdims=True)
+    bound = (BF16_HALF + 2 * e_s) * (mass + np.abs(o)) + len(rows) * 2.0 ** -23 * mass
+    if rotate_by is not None:
+        o = oracle.rope(o, -rotate_by, rope, BASE)
+        cs = np.abs(np.cos(rotate_by * oracle.rope_theta(rope, BASE)))
+        sn = np.abs(np.sin(rotate_by * oracle.rope_theta(rope, BASE)))
+        n = c - rope
+        a, b = bound[:, n::2].copy(), bound[:, n + 1::2].copy()
+        bound[:, n::2], bound[:, n + 1::2] = a * cs + b * sn, a * sn + b * cs
+    bound += BF16_HALF * np.abs(o) + 1e-30
+    err = np.abs(got - o)
+    assert np.isfinite(got).all(), what
+    assert (err <= bound).all(), (what, float((err / bound).max()))
+    assert np.linalg.norm(err) <= 2.0 ** -7 * np.linalg.norm(o) + 1e-30, (what, np.linalg.norm(err) / np.linalg.norm(o))
+
+
 class Setup:
     def __init__(self, c=512, rope=64, H=64, B=2, N=300, rpb=0, nq=1, n_win=128, W=None, seed=0, spread=0, scale=1.0,
                  win=True):
@@ -71,28 +97,7 @@ class Setup:
             if not len(rows):
                 assert not got[i].any(), f"query {i} has no rows"
                 continue
-            q = to64(self.q[i])
-            z = None if sink is None else np.asarray(sink, dtype=np.float64)
-            o = oracle.mqa_attend(q, rows, self.cfg.scale, z)
-            s = self.cfg.scale * (q @ rows.T)
-            m = s.max(1, keepdims=True) if z is None else np.maximum(s.max(1, keepdims=True), z[:, None])
-            p = np.exp(s - m)
-            p /= p.sum(1, keepdims=True) + (0 if z is None else np.exp(z[:, None] - m))
-            mass = p @ np.abs(rows)
-            e_s = 520 * 2.0 ** -24 * self.cfg.scale * (np.abs(q) @ np.abs(rows).T).max(1, keepdims=True)
-            bound = (BF16_HALF + 2 * e_s) * (mass + np.abs(o)) + len(rows) * 2.0 ** -23 * mass
-            if rotate:
-                o = oracle.rope(o, -t, self.rope, BASE)
-                cs = np.abs(np.cos(t * oracle.rope_theta(self.rope, BASE)))
-                sn = np.abs(np.sin(t * oracle.rope_theta(self.rope, BASE)))
-                n = self.c - self.rope
-                a, b = bound[:, n::2].copy(), bound[:, n + 1::2].copy()
-                bound[:, n::2], bound[:, n + 1::2] = a * cs + b * sn, a * sn + b * cs
-            bound += BF16_HALF * np.abs(o) + 1e-30
-            err = np.abs(got[i] - o)
-            assert np.isfinite(got[i]).all(), f"query {i}"
-            assert (err <= bound).all(), (i, t, float((err / bound).max()))
-            assert np.linalg.norm(err) <= 2.0 ** -7 * np.linalg.norm(o) + 1e-30, (i, t, np.linalg.norm(err) / np.linalg.norm(o))
+            check_query(got[i], to64(self.q[i]), rows, self.cfg.scale, sink, t if rotate else None, self.rope, f"query {i}")
 
 
 @pytest.mark.parametrize("H", [64, 1, 4, 16, 40, 128])
