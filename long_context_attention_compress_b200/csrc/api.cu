@@ -743,6 +743,8 @@ static KvCache kv_cache_of(const hca_kv_cache* d) {
   k.bt = d->block_table;
   k.bt_stride = d->bt_stride;
   k.rpb = d->block_table ? d->rows_per_block : 1;
+  // (a ring of 2^31 rows or more never wraps: entries are 32-bit)
+  k.div = fast_div(d->block_table ? (uint32_t)d->rows_per_block : (uint32_t)std::min(std::max(d->seq_rows, 1ll), 1ll << 31));
   k.n_req = d->n_req;
   return k;
 }
@@ -1573,7 +1575,7 @@ int kv_cache_gather(const hca_kv_cache* cache, int B, int n_out, const int32_t* 
   const char* who = "kv_cache_gather";
   const int s = check_cache(cache, who);
   if (s != HCA_OK) return s;
-  CHECK(B >= 0 && B <= cache->n_req && n_out >= 0 && (long long)B * n_out <= (1ll << 31), HCA_ERR_INVALID_ARG,
+  CHECK(B >= 0 && B <= cache->n_req && n_out >= 0 && (long long)B * n_out <= 0x7fffff00ll, HCA_ERR_INVALID_ARG,
         "%s: B=%d (cache of %d requests) n_out=%d", who, B, cache->n_req, n_out);
   CHECK(!(idx && first), HCA_ERR_INVALID_ARG, "%s: both idx and first given", who);
   CHECK(ld_out >= cache->c && ld_out % 8 == 0 && seq_stride_out >= 0 && seq_stride_out % 8 == 0, HCA_ERR_INVALID_ARG,

@@ -69,28 +69,33 @@ __device__ __forceinline__ uint32_t prmt_raw(uint32_t a, uint32_t b, uint32_t se
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
   return d;
 }
-// A whole MXFP4 block: 32 codes (16 bytes) times 2^X -> 32 bf16 as four 16-byte words, for scale bytes below 255.
-// The same byte tables, in straight-line code for every X: the multiplication is exact, or rounds to the bf16
-// subnormal or infinity that the value has (2^-127 itself is a subnormal factor, which it takes).  14 half-rate and 4
-// multiply instructions per 8 codes; the conversion instruction (E2M1 -> f16 -> f32, times 2^X, -> bf16) takes 24,
-// and mixing the two to use both pipes was slower in the attention, which is bound by issue slots.
-__device__ __forceinline__ void e2m1x32_to_bf16(const uint4& w, int X, uint4* o) {
+// The same byte tables in straight-line code for every scale byte below 255: the multiplication by 2^X is exact, or
+// rounds to the bf16 subnormal or infinity that the value has (2^-127 itself is a subnormal factor, which it takes).
+// 14 half-rate and 4 multiply instructions per 8 codes; the conversion instruction (E2M1 -> f16 -> f32, times 2^X,
+// -> bf16) takes 24, and mixing the two to use both pipes was slower in the attention, which is bound by issue slots.
+__device__ __forceinline__ uint32_t e8m0_bf16x2(uint32_t scale_byte) {  // 2^X twice, as bf16
+  const uint32_t b = scale_byte ? scale_byte << 7 : 0x0040u;
+  return b | (b << 16);
+}
+__device__ __forceinline__ uint4 e2m1x8_times(uint32_t x, uint32_t factor) {
   constexpr uint32_t kHiLo = 0x3F3F3F00u, kHiHi = 0x40404040u, kLoLo = 0xC0800000u, kLoHi = 0xC0804000u;
-  const uint32_t e = (uint32_t)(127 + X);
-  const uint32_t sb = e ? e << 7 : 0x0040u, sbits = sb | (sb << 16);  // 2^X twice, as bf16
-  const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+  const uint32_t x4 = x << 4, m = x & 0x77777777u, mh = m >> 16;
+  const uint32_t h0 = prmt_raw(kHiLo, kHiHi, m) | (prmt_raw(x4, x, 0x5140u) & 0x80808080u);
+  const uint32_t h1 = prmt_raw(kHiLo, kHiHi, mh) | (prmt_raw(x4, x, 0x7362u) & 0x80808080u);
+  const uint32_t l0 = prmt_raw(kLoLo, kLoHi, m), l1 = prmt_raw(kLoLo, kLoHi, mh);
+  uint32_t t[4] = {prmt_raw(l0, h0, 0x5140u), prmt_raw(l0, h0, 0x7362u), prmt_raw(l1, h1, 0x5140u),
+                   prmt_raw(l1, h1, 0x7362u)};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = c[i], x4 = x << 4, m = x & 0x77777777u, mh = m >> 16;
-    const uint32_t h0 = prmt_raw(kHiLo, kHiHi, m) | (prmt_raw(x4, x, 0x5140u) & 0x80808080u);
-    const uint32_t h1 = prmt_raw(kHiLo, kHiHi, mh) | (prmt_raw(x4, x, 0x7362u) & 0x80808080u);
-    const uint32_t l0 = prmt_raw(kLoLo, kLoHi, m), l1 = prmt_raw(kLoLo, kLoHi, mh);
-    uint32_t t[4] = {prmt_raw(l0, h0, 0x5140u), prmt_raw(l0, h0, 0x7362u), prmt_raw(l1, h1, 0x5140u),
-                     prmt_raw(l1, h1, 0x7362u)};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t[k]) : "r"(t[k]), "r"(sbits));
-    o[i] = make_uint4(t[0], t[1], t[2], t[3]);
-  }
+  for (int k = 0; k < 4; ++k) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t[k]) : "r"(t[k]), "r"(factor));
+  return make_uint4(t[0], t[1], t[2], t[3]);
+}
+// A whole MXFP4 block: 32 codes (16 bytes) -> 32 bf16 as four 16-byte words.
+__device__ __forceinline__ void e2m1x32_to_bf16(const uint4& w, uint32_t scale_byte, uint4* o) {
+  const uint32_t f = e8m0_bf16x2(scale_byte);
+  o[0] = e2m1x8_times(w.x, f);
+  o[1] = e2m1x8_times(w.y, f);
+  o[2] = e2m1x8_times(w.z, f);
+  o[3] = e2m1x8_times(w.w, f);
 }
 
 // Nearest E2M1 code of a (already scaled) value, ties to the even code, saturating.

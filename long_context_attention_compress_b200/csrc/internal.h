@@ -52,38 +52,6 @@ cudaError_t launch_kv_fp8_gather(const KvFp8& kv, int c, int rope_dims, int B, i
                                  int n_src, bf16* out, int32_t* idx_out, cudaStream_t stream);
 
 // ---- kv_cache.cu (rows into and out of a cache in any form) ---------------------------
-// Device form of hca_kv_cache (see hca.h).
-struct KvCache {
-  int form, c, rope_dims;
-  void* codes;
-  void* scales;
-  bf16* rope;
-  long long ld_codes, ld_scales, ld_rope;
-  long long n_rows;       // no row at or past it is touched
-  long long seq_rows;     // flat: entries a request has room for; ring: its rows
-  int ring;
-  const int32_t* bt;      // paged: request r's entry e is row bt[r*bt_stride + e/rpb]*rpb + e%rpb
-  long long bt_stride;
-  int rpb;
-  int n_req;
-};
-// Row of entry e of request `req`, or -1: an entry without room, or a block outside the pool.
-__device__ __forceinline__ long long kv_row(const KvCache& k, int req, long long e) {
-  if (e < 0 || req < 0 || req >= k.n_req) return -1;
-  long long r;
-  if (k.bt) {
-    const long long j = e / k.rpb;
-    if (j >= k.bt_stride) return -1;
-    const int blk = k.bt[req * k.bt_stride + j];
-    if (blk < 0) return -1;
-    r = (long long)blk * k.rpb + (e - j * k.rpb);
-  } else {
-    if (k.ring) e %= k.seq_rows;
-    if (e >= k.seq_rows) return -1;
-    r = req * k.seq_rows + e;
-  }
-  return r < k.n_rows ? r : -1;
-}
 // Division of 0 <= x < 2^31 by a fixed d >= 1 without a divide instruction sequence: q = floor(m x / 2^(31 + s)) with
 // m = ceil(2^(31 + s) / d), 2^(s-1) < d <= 2^s (exact for such x, since m d - 2^(31+s) < d <= 2^s).
 struct FastDiv {
@@ -99,6 +67,39 @@ inline FastDiv fast_div(uint32_t d) {
 }
 __device__ __forceinline__ uint32_t div_by(uint32_t x, const FastDiv& f) {
   return (uint32_t)(((uint64_t)x * f.m) >> 31 >> f.s);
+}
+// Device form of hca_kv_cache (see hca.h).
+struct KvCache {
+  int form, c, rope_dims;
+  void* codes;
+  void* scales;
+  bf16* rope;
+  long long ld_codes, ld_scales, ld_rope;
+  long long n_rows;       // no row at or past it is touched
+  long long seq_rows;     // flat: entries a request has room for; ring: its rows
+  int ring;
+  const int32_t* bt;      // paged: request r's entry e is row bt[r*bt_stride + e/rpb]*rpb + e%rpb
+  long long bt_stride;
+  int rpb;
+  FastDiv div;            // by rows per block (paged), by seq_rows (ring)
+  int n_req;
+};
+// Row of entry e of request `req`, or -1: an entry without room, or a block outside the pool.
+__device__ __forceinline__ long long kv_row(const KvCache& k, int req, int e) {
+  if (e < 0 || req < 0 || req >= k.n_req) return -1;
+  long long r;
+  if (k.bt) {
+    const uint32_t j = div_by(e, k.div);
+    if (j >= k.bt_stride) return -1;
+    const int blk = k.bt[req * k.bt_stride + j];
+    if (blk < 0) return -1;
+    r = (long long)blk * k.rpb + (int)(e - j * k.div.d);
+  } else {
+    if (k.ring) e -= (int)(div_by(e, k.div) * k.div.d);
+    if (e >= k.seq_rows) return -1;
+    r = req * k.seq_rows + e;
+  }
+  return r < k.n_rows ? r : -1;
 }
 struct KvAppend {
   const void* x;
@@ -326,7 +327,6 @@ struct MqaFp4Problem {
   const int32_t* q_pos;
   const int32_t* q_req;     // [Tq] or nullptr: query i belongs to request i
   int Tq, H;
-  FastDiv rpb;              // (set by launch_mqa_fp4)
   float scale;
   const float* sink;
   int rope_dims;            // > 0: the output's last rope_dims channels turn back by -q_pos

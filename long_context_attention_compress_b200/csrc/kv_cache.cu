@@ -9,13 +9,19 @@
 // rows (c*4 B in, 366 B out for FP4 at c = 512), by latency for few.
 // Roundings.  With normalisation or rotation y is rounded to bf16 first (what the bf16 cache holds), as from the
 // float64 value: a quantised code must not depend on which side of a midpoint an f32 normalisation falls.  Sum of
-// squares and rotation are f64; the other channels are formed in f32 and redone in f64 only within 16 f32 ulps of a
-// bf16 midpoint (f32 is within 3).  The codes are those of the stored-form definitions bit for bit: FP4 scaling is
+// squares and rotation are f64; the other channels are formed in f32, 8 ulps too low and too high (f32 is within 4),
+// and redone in f64 only where the two round apart.  The codes are those of the stored-form definitions bit for bit: FP4 scaling is
 // exact and the conversion rounds to nearest even; an f32 quotient within 4 ulps of an E4M3 midpoint, or in E4M3's
 // subnormal range, is decided on the f64 quotient.
 //
-// kv_gather_kernel.  The bf16 values of rows; one warp a row, four rows in flight per warp (each row is a chain of
-// dependent loads: index, block table, row).
+// The angle is formed in turns from theta / 2 pi in two f64 words (a table made on the host) with an error-free product,
+// so that its fraction is good to 2^-52 at any position and the sine and cosine need no long reduction.
+//
+// kv_gather_kernel.  The bf16 values of rows.  Each row is a chain of dependent loads (index, block table, row): a block
+// resolves 32 rows at a time, one a thread, while its warps move the 32 before, four rows in flight per warp.
+
+#include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "formats.cuh"
@@ -58,48 +64,107 @@ __device__ __forceinline__ uint32_t e2m1x8_encode(const float* y) {
   return w & (0x77777777u | (mag << 3));
 }
 
-// Two E4M3 codes of y / sc (see the head of this file).
+// Eight E4M3 codes of y / sc (see the head of this file).  The f64 decision is rare and long: one call outside the
+// straight line, for the elements that need it.
 __device__ __forceinline__ bool e4m3_doubtful(float q) {
   const int low = (int)(__float_as_uint(q) & 0xfffffu) - 0x80000;
   return !(fabsf(q) >= 0.015625f) || (low >= -4 && low <= 4);
 }
-__device__ __forceinline__ uint32_t e4m3x2_encode(float y0, float y1, float sc) {
-  const float q0 = y0 / sc, q1 = y1 / sc;
-  uint16_t h;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(q1), "f"(q0));
-  uint32_t w = h;
-  if (e4m3_doubtful(q0)) w = (w & 0xff00u) | e4m3_encode((double)y0 / (double)sc);
-  if (e4m3_doubtful(q1)) w = (w & 0x00ffu) | (e4m3_encode((double)y1 / (double)sc) << 8);
-  return w;
+__device__ __noinline__ uint32_t e4m3_decide(float y, float sc) { return e4m3_encode((double)y / (double)sc); }
+__device__ __forceinline__ uint2 e4m3x8_encode(const float* y, float sc) {
+  uint32_t w[4];
+  uint32_t doubt = 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const float q0 = y[2 * t] / sc, q1 = y[2 * t + 1] / sc;
+    uint16_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(q1), "f"(q0));
+    w[t] = h;
+    doubt |= (e4m3_doubtful(q0) ? 1u << (2 * t) : 0u) | (e4m3_doubtful(q1) ? 2u << (2 * t) : 0u);
+  }
+  uint2 r = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  while (doubt) {
+    const int t = __ffs(doubt) - 1;
+    doubt &= doubt - 1;
+    float v = y[0];
+#pragma unroll
+    for (int u = 1; u < 8; ++u) v = t == u ? y[u] : v;
+    const uint32_t c = e4m3_decide(v, sc), sh = 8 * (t & 3);
+    if (t < 4) r.x = (r.x & ~(255u << sh)) | (c << sh);
+    else r.y = (r.y & ~(255u << sh)) | (c << sh);
+  }
+  return r;
 }
 
-template <bool F32, int FORM>
-__global__ void __launch_bounds__(32 * kKvWarps) kv_append_kernel(KvAppend a, KvCache k, int rows_per_warp) {
-  __shared__ double2 s_cs[kKvWarps][kKvMaxPairs];  // cosine and sine of each pair at the warp's current position
-  const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5;
-  const int r0 = (blockIdx.x * kKvWarps + wib) * rows_per_warp;
-  const int r1 = min(a.n_rows, r0 + rows_per_warp);
+// theta_j / 2 pi = base^(-2j / rope_dims) / 2 pi of each pair, as the sum of two doubles.
+struct Turns {
+  double hi[kKvMaxPairs], lo[kKvMaxPairs];
+};
+
+// Resident blocks per SM that the registers are held to.
+constexpr int append_blocks(int form, bool xf) { return xf ? 6 : form == HCA_KV_FP8 ? 8 : 10; }
+
+// XF: with normalisation or rotation; without, a row is only converted.  LANES lanes a row: 16 for rows of at most 128
+// channels that are only converted (the indexer's keys), else 32.
+template <bool F32, int FORM, bool XF, int LANES>
+__global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
+    kv_append_kernel(KvAppend a, KvCache k, int rows_per_group, const __grid_constant__ Turns turns) {
+  constexpr int kU = LANES == 32 ? kKvChunks : 1;  // chunks per lane
+  __shared__ double2 s_cs[XF ? kKvWarps : 1][kKvMaxPairs];  // cosine and sine of each pair at the warp's position
+  const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, sub = lane & (LANES - 1);
+  const unsigned int all = LANES == 32 ? 0xffffffffu : 0xffffu << (lane & 16);  // this row's lanes
+  const int r0 = ((blockIdx.x * kKvWarps + wib) * (32 / LANES) + lane / LANES) * rows_per_group;
+  const int r1 = min(a.n_rows, r0 + rows_per_group);
   if (r0 >= r1) return;
   const int nch = k.c >> 3;
   const int rope0 = k.c - k.rope_dims;
-  const int n_pairs = a.rotate ? k.rope_dims >> 1 : 0;
-  double theta[kKvMaxPairs / 32];
+  const int n_pairs = XF && a.rotate ? k.rope_dims >> 1 : 0;
+  double turn_hi[kKvMaxPairs / 32], turn_lo[kKvMaxPairs / 32];  // of pairs lane, lane + 32, ...
+  if constexpr (XF) {
 #pragma unroll
-  for (int u = 0; u < kKvMaxPairs / 32; ++u)
-    theta[u] = lane + 32 * u < n_pairs ? pow((double)a.rope_base, -2.0 * (lane + 32 * u) / k.rope_dims) : 0.0;
-  // request of the first row: the last one that starts at or before it
+    for (int u = 0; u < kKvMaxPairs / 32; ++u) {
+      turn_hi[u] = lane + 32 * u < n_pairs ? turns.hi[lane + 32 * u] : 0.0;
+      turn_lo[u] = lane + 32 * u < n_pairs ? turns.lo[lane + 32 * u] : 0.0;
+    }
+  }
+  const double inv_c = 1.0 / k.c;
+  // The next row is always under way: its load depends on nothing else.
+  float next[kU][8];
+  auto load_row = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int ch = sub + LANES * u;
+      if (ch < nch) {
+        load8<F32>(a.x, (long long)i * a.ld_x + ch * 8, next[u]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) next[u][t] = 0.f;
+      }
+    }
+  };
+  load_row(r0);
+  // Request of the first row: the last one that starts at or before it, by a search as wide as the row's lanes.
   int b = r0, start = r0, end = r0 + 1;
   if (a.row_start) {
     int lo = 0, hi = a.B;  // row_start[lo] <= r0 < row_start[hi], if anywhere
     while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.row_start[mid] <= r0) lo = mid; else hi = mid;
+      const int step = (hi - lo + LANES - 1) / LANES, m = min(lo + sub * step, hi - 1);
+      const unsigned int at = (__ballot_sync(all, sub == 0 || a.row_start[m] <= r0) & all) >> (lane & (32 - LANES));
+      const int last = 31 - __clz(at);
+      hi = min(hi, lo + (last + 1) * step);
+      lo = min(lo + last * step, hi - 1);
     }
     b = lo;
     start = a.row_start[b];
     end = a.row_start[b + 1];
   }
   for (int i = r0; i < r1; ++i) {
+    float v[kU][8];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int t = 0; t < 8; ++t) v[u][t] = next[u][t];
+    if (i + 1 < r1) load_row(i + 1);
     if (a.row_start) {
       while (i >= end && b + 1 < a.B) {
         ++b;
@@ -116,51 +181,42 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv_append_kernel(KvAppend a, Kv
     const long long e = (long long)f + (i - start);
     if (f < 0) continue;
     if (k.ring && (long long)end - i > k.seq_rows) continue;  // a later row of this call takes its place
-    const long long row = kv_row(k, b, e);
+    const long long row = e <= 0x7fffffffll ? kv_row(k, b, (int)e) : -1;
     if (row < 0) {
-      if (a.check && lane == 0) atomicOr(&g_kv_append_error, 1u);
+      if (a.check && sub == 0) atomicOr(&g_kv_append_error, 1u);
       continue;
     }
-    float v[kKvChunks][8];
+    if constexpr (XF) {
+      if (n_pairs > 0) {
+        const double pos = (double)((e + 1) * a.rate - 1);
+        __syncwarp();  // the last row's table has been read
 #pragma unroll
-    for (int u = 0; u < kKvChunks; ++u) {
-      const int ch = lane + 32 * u;
-      if (ch < nch) {
-        load8<F32>(a.x, (long long)i * a.ld_x + ch * 8, v[u]);
-      } else {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) v[u][t] = 0.f;
-      }
-    }
-    if (n_pairs > 0) {
-      const double pos = (double)((e + 1) * a.rate - 1);
-      __syncwarp();  // the last row's table has been read
-#pragma unroll
-      for (int u = 0; u < kKvMaxPairs / 32; ++u) {
-        if (lane + 32 * u < n_pairs) {
-          double sn, cs;
-          sincos(pos * theta[u], &sn, &cs);
-          s_cs[wib][lane + 32 * u] = make_double2(cs, sn);
+        for (int u = 0; u < kKvMaxPairs / 32; ++u) {
+          if (lane + 32 * u < n_pairs) {
+            const double t = pos * turn_hi[u];
+            const double rest = fma(pos, turn_lo[u], fma(pos, turn_hi[u], -t));  // what t lacks
+            double sn, cs;
+            sincospi(2.0 * ((t - rint(t)) + rest), &sn, &cs);
+            s_cs[wib][lane + 32 * u] = make_double2(cs, sn);
+          }
         }
+        __syncwarp();
       }
-      __syncwarp();
-    }
-    if (a.gamma || n_pairs > 0) {
       double inv = 1.0;
       if (a.gamma) {
         double ss = 0.0;
 #pragma unroll
-        for (int u = 0; u < kKvChunks; ++u)
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int t = 0; t < 8; ++t) ss = fma((double)v[u][t], (double)v[u][t], ss);
 #pragma unroll
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        inv = rsqrt(ss / k.c + (double)a.eps);
+        inv = rsqrt(fma(ss, inv_c, (double)a.eps));
       }
-      const float inv32 = (float)inv;
+      const float inv_lo = (float)inv * (1.f - 0x1p-21f), inv_hi = (float)inv * (1.f + 0x1p-21f);
 #pragma unroll
-      for (int u = 0; u < kKvChunks; ++u) {
-        const int ch = lane + 32 * u;
+      for (int u = 0; u < kU; ++u) {
+        const int ch = sub + LANES * u;
         if (ch >= nch) continue;
         float g[8];
         if (a.gamma) {
@@ -180,29 +236,47 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv_append_kernel(KvAppend a, Kv
             v[u][2 * t + 1] = (float)(p * r.y + q * r.x);
           }
         } else if (a.gamma) {
+          // The value lies between these two f32 products, 8 ulps apart either way; where both round to one bf16, so
+          // does it.
+          uint32_t w[4], differ = 0;
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            float y = v[u][t] * inv32 * g[t];
-            const int low = (int)(__float_as_uint(y) & 0xffffu) - 0x8000;  // 0: a bf16 midpoint
-            if (low > -16 && low < 16) y = (float)((double)v[u][t] * inv * (double)g[t]);
-            v[u][t] = y;
+          for (int t = 0; t < 4; ++t) {
+            const float y0 = v[u][2 * t] * g[2 * t], y1 = v[u][2 * t + 1] * g[2 * t + 1];
+            w[t] = pack_bf16x2(y0 * inv_lo, y1 * inv_lo);
+            differ |= w[t] ^ pack_bf16x2(y0 * inv_hi, y1 * inv_hi);
           }
+          if (differ) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              w[t] = pack_bf16x2((float)((double)v[u][2 * t] * inv * (double)g[2 * t]),
+                                 (float)((double)v[u][2 * t + 1] * inv * (double)g[2 * t + 1]));
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            v[u][2 * t] = bf16_lo(w[t]);
+            v[u][2 * t + 1] = bf16_hi(w[t]);
+          }
+          continue;
         }
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[u][t] = __bfloat162float(__float2bfloat16_rn(v[u][t]));
+        for (int t = 0; t < 8; t += 2) {
+          const uint32_t w = pack_bf16x2(v[u][t], v[u][t + 1]);
+          v[u][t] = bf16_lo(w);
+          v[u][t + 1] = bf16_hi(w);
+        }
       }
     }
     // the row in the cache's form
 #pragma unroll
-    for (int u = 0; u < kKvChunks; ++u) {
-      const int ch = lane + 32 * u;
+    for (int u = 0; u < kU; ++u) {
+      const int ch = sub + LANES * u;
       float amax = 0.f;
       if constexpr (FORM != HCA_KV_BF16) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) amax = fmaxf(amax, fabsf(v[u][t]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        if constexpr (FORM == HCA_KV_FP8) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+        amax = fmaxf(amax, __shfl_xor_sync(all, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(all, amax, 2));
+        if constexpr (FORM == HCA_KV_FP8) amax = fmaxf(amax, __shfl_xor_sync(all, amax, 4));
       }
       if (ch >= nch) continue;
       const int d = ch * 8;
@@ -214,20 +288,20 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv_append_kernel(KvAppend a, Kv
         *reinterpret_cast<uint4*>(dst) = w;
       } else if constexpr (FORM == HCA_KV_FP8) {
         const float sc = amax > 0.f ? amax / 448.f : 1.f;
-        uint2 w;
-        w.x = e4m3x2_encode(v[u][0], v[u][1], sc) | (e4m3x2_encode(v[u][2], v[u][3], sc) << 16);
-        w.y = e4m3x2_encode(v[u][4], v[u][5], sc) | (e4m3x2_encode(v[u][6], v[u][7], sc) << 16);
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(k.codes) + row * k.ld_codes + d) = w;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(k.codes) + row * k.ld_codes + d) =
+            e4m3x8_encode(v[u], sc);
         if ((ch & 7) == 0) reinterpret_cast<float*>(k.scales)[row * k.ld_scales + ch / 8] = sc;
       } else if constexpr (FORM == HCA_KV_FP4) {
-        const int X = mx_exponent(amax);
-        const float down = __uint_as_float(X < 127 ? (uint32_t)(127 - X) << 23 : 0x00400000u);  // 2^-X
+        // scale byte X + 127, X = floor(log2 amax) - 2 in [-127, 127] (an amax of zero or a subnormal gives -127, an
+        // infinite one 127), and 2^-X
+        const uint32_t ex = __float_as_uint(amax) >> 23, sb = ex == 255u ? 254u : ex > 2u ? ex - 2u : 0u;
+        const float down = __uint_as_float(sb < 254u ? (254u - sb) << 23 : 0x00400000u);
         float y[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) y[t] = v[u][t] * down;
         *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(k.codes) + row * k.ld_codes + d / 2) =
             e2m1x8_encode(y);
-        if ((ch & 3) == 0) reinterpret_cast<uint8_t*>(k.scales)[row * k.ld_scales + ch / 4] = (uint8_t)(X + 127);
+        if ((ch & 3) == 0) reinterpret_cast<uint8_t*>(k.scales)[row * k.ld_scales + ch / 4] = (uint8_t)sb;
       }
     }
   }
@@ -240,107 +314,173 @@ __device__ __forceinline__ float e4m3_scaled(uint32_t b, float sc) {
   return ((b & 0x80u) ? -mag : mag) * sc;
 }
 
-constexpr int kGatherRows = 4;  // rows in flight per warp
+// Loads that are made or not (zeros) without a branch, so that a batch of them is under way at once.
+__device__ __forceinline__ uint4 load16_if(const void* p, bool ok) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(ok ? 1 : 0));
+  return v;
+}
+__device__ __forceinline__ uint2 load8_if(const void* p, bool ok) {
+  uint2 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+      "@p ld.global.v2.b32 {%0, %1}, [%2];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y)
+      : "l"(p), "r"(ok ? 1 : 0));
+  return v;
+}
+__device__ __forceinline__ uint32_t load4_if(const void* p, bool ok) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.b32 %0, [%1];\n\t}"
+               : "=&r"(v)
+               : "l"(p), "r"(ok ? 1 : 0));
+  return v;
+}
+__device__ __forceinline__ uint32_t load1_if(const void* p, bool ok) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.u8 %0, [%1];\n\t}"
+               : "=&r"(v)
+               : "l"(p), "r"(ok ? 1 : 0));
+  return v;
+}
+
+constexpr int kGatherRows = 4;                       // rows in flight per warp
+constexpr int kGatherBlock = 8 * kGatherRows;        // rows a block takes at a time
+constexpr int kGatherResident = 3;                   // blocks per SM
 
 template <int FORM>
-__global__ void __launch_bounds__(256) kv_gather_kernel(KvCache k, int n_out, long long total,
+__global__ void __launch_bounds__(256, kGatherResident) kv_gather_kernel(KvCache k, FastDiv n_out, uint32_t total,
                                                         const int32_t* __restrict__ idx,
                                                         const int32_t* __restrict__ first, bf16* __restrict__ out,
                                                         long long ld_out, long long seq_out) {
-  const int lane = threadIdx.x & 31;
-  const long long w0 = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
+  __shared__ long long s_row[2][kGatherBlock], s_dst[2][kGatherBlock];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nch = k.c >> 3;
   const int rope0 = k.c - k.rope_dims;
-  long long row[kGatherRows], dst[kGatherRows];
-#pragma unroll
-  for (int r = 0; r < kGatherRows; ++r) {
-    const long long o = w0 * kGatherRows + r;
-    row[r] = -1;
-    dst[r] = -1;
-    if (o < total) {
-      const int b = (int)(o / n_out), j = (int)(o % n_out);
-      long long e = j;
-      if (idx) {
-        e = idx[o];
-      } else if (first) {
-        const int f = first[b];
-        e = f < 0 ? -1 : (long long)f + j;
-      }
-      row[r] = kv_row(k, b, e);
-      dst[r] = b * seq_out + j * ld_out;
+  // Where row o comes from and goes to: one row a thread, 32 dependent chains side by side.
+  auto resolve = [&](uint32_t o, int buf) {
+    const int b = (int)div_by(o, n_out), j = (int)(o - b * n_out.d);
+    int e = j;
+    if (idx) {
+      e = idx[o];
+    } else if (first) {
+      const int f = first[b];
+      e = f < 0 || f > 0x7fffffff - j ? -1 : f + j;
     }
-  }
+    s_row[buf][threadIdx.x] = kv_row(k, b, e);
+    s_dst[buf][threadIdx.x] = b * seq_out + j * ld_out;
+  };
+  const uint32_t stride = gridDim.x * kGatherBlock;
+  uint32_t base = blockIdx.x * kGatherBlock;
+  if (threadIdx.x < kGatherBlock && base + threadIdx.x < total) resolve(base + threadIdx.x, 0);
+  __syncthreads();
+  for (int buf = 0; base < total; base += stride, buf ^= 1) {
+    // (total < 2^31 and the stride is a few thousand rows a time: no overflow)
+    if (threadIdx.x < kGatherBlock && base + stride + threadIdx.x < total) resolve(base + stride + threadIdx.x, buf ^ 1);
+    {
+      const int s0 = warp * kGatherRows;
+      long long row[kGatherRows];
+      uint4 raw[kKvChunks][kGatherRows];
+      uint32_t sc[kKvChunks][kGatherRows];
 #pragma unroll
-  for (int u = 0; u < kKvChunks; ++u) {
-    const int ch = lane + 32 * u, d = ch * 8;
-    if (ch >= nch) continue;
-    const bool wide = FORM == HCA_KV_BF16 || d >= rope0;
-    uint4 raw[kGatherRows];
-    uint32_t sc[kGatherRows];
+      for (int r = 0; r < kGatherRows; ++r) row[r] = base + s0 + r < total ? s_row[buf][s0 + r] : -1;
 #pragma unroll
-    for (int r = 0; r < kGatherRows; ++r) {
-      raw[r] = make_uint4(0u, 0u, 0u, 0u);
-      sc[r] = 0u;
-      if (row[r] < 0) continue;
-      if (wide) {
-        raw[r] = *reinterpret_cast<const uint4*>(
-            FORM == HCA_KV_BF16 ? reinterpret_cast<const bf16*>(k.codes) + row[r] * k.ld_codes + d
-                                : k.rope + row[r] * k.ld_rope + (d - rope0));
-      } else if constexpr (FORM == HCA_KV_FP8) {
-        const uint2 t = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(k.codes) +
-                                                        row[r] * k.ld_codes + d);
-        raw[r].x = t.x;
-        raw[r].y = t.y;
-        sc[r] = __float_as_uint(reinterpret_cast<const float*>(k.scales)[row[r] * k.ld_scales + ch / 8]);
-      } else if constexpr (FORM == HCA_KV_FP4) {
-        raw[r].x = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(k.codes) +
-                                                      row[r] * k.ld_codes + d / 2);
-        sc[r] = reinterpret_cast<const uint8_t*>(k.scales)[row[r] * k.ld_scales + ch / 4];
-      }
-    }
+      for (int u = 0; u < kKvChunks; ++u) {
+        const int ch = lane + 32 * u, d = ch * 8;
+        const bool wide = FORM == HCA_KV_BF16 || d >= rope0;
 #pragma unroll
-    for (int r = 0; r < kGatherRows; ++r) {
-      if (dst[r] < 0) continue;
-      uint4 w = raw[r];
-      if (!wide && row[r] >= 0) {
-        if constexpr (FORM == HCA_KV_FP8) {
-          const float s = __uint_as_float(sc[r]);
-          const uint32_t lo = raw[r].x, hi = raw[r].y;
-          w.x = pack_bf16x2(e4m3_scaled(lo, s), e4m3_scaled(lo >> 8, s));
-          w.y = pack_bf16x2(e4m3_scaled(lo >> 16, s), e4m3_scaled(lo >> 24, s));
-          w.z = pack_bf16x2(e4m3_scaled(hi, s), e4m3_scaled(hi >> 8, s));
-          w.w = pack_bf16x2(e4m3_scaled(hi >> 16, s), e4m3_scaled(hi >> 24, s));
-        } else if constexpr (FORM == HCA_KV_FP4) {
-          uint32_t o[4];
-          e2m1x8_to_bf16(raw[r].x, (int)sc[r] - 127, o);
-          w = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int r = 0; r < kGatherRows; ++r) {
+          const bool ok = row[r] >= 0 && ch < nch;
+          const uint8_t* code = reinterpret_cast<const uint8_t*>(k.codes);
+          if constexpr (FORM == HCA_KV_BF16) {
+            raw[u][r] = load16_if(code + (row[r] * k.ld_codes + d) * 2, ok);
+          } else {
+            // lanes of the rotary channels load 16 bytes, the others their codes and scale
+            const uint4 w = load16_if(k.rope + row[r] * k.ld_rope + (d - rope0), ok && wide);
+            if constexpr (FORM == HCA_KV_FP8) {
+              const uint2 t = load8_if(code + row[r] * k.ld_codes + d, ok && !wide);
+              raw[u][r] = wide ? w : make_uint4(t.x, t.y, 0u, 0u);
+              sc[u][r] = load4_if(reinterpret_cast<const float*>(k.scales) + row[r] * k.ld_scales + ch / 8, ok && !wide);
+            } else {
+              const uint32_t t = load4_if(code + row[r] * k.ld_codes + d / 2, ok && !wide);
+              raw[u][r] = wide ? w : make_uint4(t, 0u, 0u, 0u);
+              sc[u][r] = load1_if(reinterpret_cast<const uint8_t*>(k.scales) + row[r] * k.ld_scales + ch / 4, ok && !wide);
+            }
+          }
         }
       }
-      *reinterpret_cast<uint4*>(out + dst[r] + d) = w;
+#pragma unroll
+      for (int u = 0; u < kKvChunks; ++u) {
+        const int ch = lane + 32 * u, d = ch * 8;
+        const bool wide = FORM == HCA_KV_BF16 || d >= rope0;
+#pragma unroll
+        for (int r = 0; r < kGatherRows; ++r) {
+          if (base + s0 + r >= total || ch >= nch) continue;
+          uint4 w = raw[u][r];
+          if (!wide && row[r] >= 0) {
+            if constexpr (FORM == HCA_KV_FP8) {
+              const float s = __uint_as_float(sc[u][r]);
+              const uint32_t lo = raw[u][r].x, hi = raw[u][r].y;
+              w.x = pack_bf16x2(e4m3_scaled(lo, s), e4m3_scaled(lo >> 8, s));
+              w.y = pack_bf16x2(e4m3_scaled(lo >> 16, s), e4m3_scaled(lo >> 24, s));
+              w.z = pack_bf16x2(e4m3_scaled(hi, s), e4m3_scaled(hi >> 8, s));
+              w.w = pack_bf16x2(e4m3_scaled(hi >> 16, s), e4m3_scaled(hi >> 24, s));
+            } else if constexpr (FORM == HCA_KV_FP4) {
+              w = e2m1x8_times(raw[u][r].x, e8m0_bf16x2(sc[u][r]));
+            }
+          }
+          *reinterpret_cast<uint4*>(out + s_dst[buf][s0 + r] + d) = w;
+        }
+      }
     }
+    __syncthreads();
   }
+}
+
+// The table for the last base and number of rotary channels used on this thread.
+const Turns& turns_of(int rope_dims, float base) {
+  static thread_local Turns t;
+  static thread_local int have_dims = 0;
+  static thread_local float have_base = 0.f;
+  if (rope_dims != have_dims || base != have_base) {
+    const long double two_pi = 2.0L * acosl(-1.0L);
+    for (int j = 0; j < rope_dims / 2; ++j) {
+      const long double v = powl((long double)base, -2.0L * j / rope_dims) / two_pi;
+      t.hi[j] = (double)v;
+      t.lo[j] = (double)(v - (long double)t.hi[j]);
+    }
+    have_dims = rope_dims;
+    have_base = base;
+  }
+  return t;
 }
 }  // namespace
 
-template <bool F32>
-static void append_form(const KvAppend& a, const KvCache& k, unsigned grid, int per, cudaStream_t stream) {
-  if (k.form == HCA_KV_BF16)
-    kv_append_kernel<F32, HCA_KV_BF16><<<grid, 32 * kKvWarps, 0, stream>>>(a, k, per);
-  else if (k.form == HCA_KV_FP8)
-    kv_append_kernel<F32, HCA_KV_FP8><<<grid, 32 * kKvWarps, 0, stream>>>(a, k, per);
-  else
-    kv_append_kernel<F32, HCA_KV_FP4><<<grid, 32 * kKvWarps, 0, stream>>>(a, k, per);
+template <bool F32, int FORM>
+static void append_rows(const KvAppend& a, const KvCache& k, cudaStream_t stream) {
+  const bool xf = a.gamma || (a.rotate && k.rope_dims > 0);
+  const Turns& turns = turns_of(a.rotate ? k.rope_dims : 0, a.rope_base);
+  // one row a group of lanes until the machine is full (the resident warps of the launch bounds), then contiguous runs
+  const int groups = !xf && k.c <= 128 ? 2 : 1;  // per warp
+  const int max_groups = device_sm_count() * kKvWarps * append_blocks(FORM, xf) * groups;
+  const int per = (a.n_rows + max_groups - 1) / max_groups;
+  const int blocks = (a.n_rows + per * kKvWarps * groups - 1) / (per * kKvWarps * groups);
+  const dim3 block(32 * kKvWarps);
+  if (xf) kv_append_kernel<F32, FORM, true, 32><<<blocks, block, 0, stream>>>(a, k, per, turns);
+  else if (groups == 1) kv_append_kernel<F32, FORM, false, 32><<<blocks, block, 0, stream>>>(a, k, per, turns);
+  else kv_append_kernel<F32, FORM, false, 16><<<blocks, block, 0, stream>>>(a, k, per, turns);
 }
 
 cudaError_t launch_kv_append(const KvAppend& a, const KvCache& k, cudaStream_t stream) {
   if (a.n_rows <= 0 || a.B <= 0) return cudaSuccess;
-  // one row a warp until the machine is full (32 warps per SM), then contiguous runs
-  const int max_warps = device_sm_count() * 32;
-  const int per = (a.n_rows + max_warps - 1) / max_warps;
-  const int warps = (a.n_rows + per - 1) / per;
-  const unsigned grid = (unsigned)((warps + kKvWarps - 1) / kKvWarps);
-  if (a.x_f32) append_form<true>(a, k, grid, per, stream);
-  else append_form<false>(a, k, grid, per, stream);
+  if (k.form == HCA_KV_BF16) a.x_f32 ? append_rows<true, HCA_KV_BF16>(a, k, stream) : append_rows<false, HCA_KV_BF16>(a, k, stream);
+  else if (k.form == HCA_KV_FP8) a.x_f32 ? append_rows<true, HCA_KV_FP8>(a, k, stream) : append_rows<false, HCA_KV_FP8>(a, k, stream);
+  else a.x_f32 ? append_rows<true, HCA_KV_FP4>(a, k, stream) : append_rows<false, HCA_KV_FP4>(a, k, stream);
   ++g_launch_counter;
   return cudaGetLastError();
 }
@@ -349,13 +489,15 @@ cudaError_t launch_kv_gather(const KvCache& k, int B, int n_out, const int32_t* 
                              long long ld_out, long long seq_out, cudaStream_t stream) {
   const long long total = (long long)B * n_out;
   if (total <= 0) return cudaSuccess;
-  const unsigned grid = (unsigned)((total + 8 * kGatherRows - 1) / (8 * kGatherRows));
+  const unsigned grid = (unsigned)std::min<long long>((total + kGatherBlock - 1) / kGatherBlock, (long long)kGatherResident * device_sm_count());
+  const FastDiv n = fast_div((uint32_t)n_out);
+  const uint32_t rows = (uint32_t)total;
   if (k.form == HCA_KV_BF16)
-    kv_gather_kernel<HCA_KV_BF16><<<grid, 256, 0, stream>>>(k, n_out, total, idx, first, out, ld_out, seq_out);
+    kv_gather_kernel<HCA_KV_BF16><<<grid, 256, 0, stream>>>(k, n, rows, idx, first, out, ld_out, seq_out);
   else if (k.form == HCA_KV_FP8)
-    kv_gather_kernel<HCA_KV_FP8><<<grid, 256, 0, stream>>>(k, n_out, total, idx, first, out, ld_out, seq_out);
+    kv_gather_kernel<HCA_KV_FP8><<<grid, 256, 0, stream>>>(k, n, rows, idx, first, out, ld_out, seq_out);
   else
-    kv_gather_kernel<HCA_KV_FP4><<<grid, 256, 0, stream>>>(k, n_out, total, idx, first, out, ld_out, seq_out);
+    kv_gather_kernel<HCA_KV_FP4><<<grid, 256, 0, stream>>>(k, n, rows, idx, first, out, ld_out, seq_out);
   ++g_launch_counter;
   return cudaGetLastError();
 }

@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     // The block that entry e lies in (paged), loaded but not looked at yet, and its cache row from it.
     auto block_of = [&](int e) -> int {
       if (!p.kv.bt || e < 0 || e >= p.N) return 0;
-      const unsigned int j = div_by(e, p.rpb);
+      const unsigned int j = div_by(e, p.kv.div);
       return j < p.kv.bt_stride ? p.kv.bt[r.req * p.kv.bt_stride + j] : -1;
     };
     auto resolve = [&](int lt, int e, int blk) -> int {
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
         if (k) atomicOr(&g_mqa_fp4_error, k << 1);
       }
       if (e < 0 || e >= p.N) return -1;
-      long long x = p.kv.bt ? (blk < 0 ? -1ll : (long long)blk * p.kv.rpb + (e - (int)(div_by(e, p.rpb) * p.rpb.d)))
+      long long x = p.kv.bt ? (blk < 0 ? -1ll : (long long)blk * p.kv.rpb + (e - (int)(div_by(e, p.kv.div) * p.kv.div.d)))
                             : (e < p.kv.seq_rows ? r.req * p.kv.seq_rows + e : -1ll);
       if (x >= p.kv.n_rows) x = -1;
       if (p.check && x < 0) atomicOr(&g_mqa_fp4_error, kIdxBlock << 1);
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     if (rope64 && la < le) copy_rope(i, x);  // (PV of tile i-2 has released this buffer)
     // Widen this thread's group of block b (one that is not held in 4 bits: its codes are zeros).
     auto widen = [&](int b, const uint4& v, uint32_t scale_word, uint4 (&o)[4]) {
-      e2m1x32_to_bf16(v, (int)((scale_word >> (8 * sub)) & 255u) - 127, o);
+      e2m1x32_to_bf16(v, (scale_word >> (8 * sub)) & 255u, o);
     };
     // Store a widened group of block b and signal the block.
     auto put = [&](int i, int b, const uint4 (&o)[4]) {
@@ -877,10 +877,8 @@ static cudaError_t launch_tc(const MqaFp4Problem& p, int pack, int splits, float
   return cudaGetLastError();
 }
 
-cudaError_t launch_mqa_fp4(const MqaFp4Problem& problem, const MqaPlan& pl, void* ws, cudaStream_t stream) {
-  if (problem.Tq == 0) return cudaSuccess;
-  MqaFp4Problem p = problem;
-  p.rpb = fast_div((uint32_t)p.kv.rpb);
+cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, cudaStream_t stream) {
+  if (p.Tq == 0) return cudaSuccess;
   float* ws_o = reinterpret_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)p.Tq * pl.splits * p.H * p.kv.c);
   cudaError_t e;
