@@ -1601,7 +1601,8 @@ static MqaPlan fp4_plan(const hca_layer_cfg* cfg, int Tq, int N, int n_idx, bool
 // Whether the queries name their requests or not.
 static size_t fp4_ws(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
   if (Tq == 0) return 0;
-  return round256(std::max(fp4_plan(cfg, Tq, N, n_idx, false).ws_bytes, fp4_plan(cfg, Tq, N, n_idx, true).ws_bytes));
+  const size_t one = fp4_plan(cfg, Tq, N, n_idx, false).ws_bytes;
+  return round256(n_idx || Tq == 1 ? one : std::max(one, fp4_plan(cfg, Tq, N, n_idx, true).ws_bytes));
 }
 
 size_t sparse_mqa_attend_fp4_workspace(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {

@@ -227,6 +227,14 @@ __device__ __forceinline__ float warp_sum16(float (&a)[16], int lane) {
   rs_sum_step<1, 2>(a, lane);
   return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 16);
 }
+// Whether one of eight bf16 values is an infinity or a NaN.
+__device__ __forceinline__ bool any_not_finite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool r = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+  return r;
+}
 __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
@@ -409,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       const bool lead = tc::elect_one();
       if (lead) {
         tc::mbar_arrive_expect_tx(&bars->qfull, kQBytes);
-        for (int ch = 0; ch < 8; ++ch) tc::tma_load_3d(base + kOffQ + ch * kQChunk, &tm_q, &bars->qfull, ch * 64, PACK ? q0 * p.H : h0, PACK ? 0 : q0);
+        for (int ch = 0; ch < 8; ++ch)
+          tc::tma_load_3d(base + kOffQ + ch * kQChunk, &tm_q, &bars->qfull, ch * 64, PACK ? q0 * p.H : h0, PACK ? 0 : q0);
       }
       __syncwarp();
       constexpr uint32_t id_qk = tc::idesc_bf16_f32(kRowsT, kHT, false, false);
@@ -485,149 +494,178 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     // Columns are taken 16 at a time, to keep the registers of a thread few.
     float lw = 0.f;  // lane l: column 32 hsel + l's sum over this warp's rows, relative to the running maximum
     unsigned char* prow = base + kOffP + row * 128;
+    // 128-byte part of this row of tile i in chunk ch.
+    auto row_part = [&](int i, int ch) -> uint4* {
+      return reinterpret_cast<uint4*>(base + kOffKv + ch * kKvChunk + (ch == 7 && (i & 1) ? kR2Delta : 0u) + row * 128);
+    };
     bool failed = false;
     int i = 0, g = 0;
     for (int j = 0; j < grp.n && !failed;) {
-     const Run r = grp.run(p, j, lane);
-     j = r.j1;
-     const int la = max(ga - g, 0), lb = min(gb - g, r.n);
-     g += r.n;
-     // packed: the rows that column 32 hsel + lane sees: entries below ecount; window tokens wlo .. wlo + wcount - 1
-     int ecount = 0, wlo = 0, wcount = 0;
-     if (PACK) {
-       const int jc = (32 * hsel + lane) / p.H;
-       const int tc_ = __shfl_sync(0xffffffffu, grp.t, min(jc, 31)), vc = __shfl_sync(0xffffffffu, grp.vis, min(jc, 31));
-       if (jc >= r.j0 && jc < r.j1) {
-         ecount = vc;
-         wlo = max(0, tc_ - p.n_win + 1);
-         wcount = tc_ - wlo + 1;
-       }
-     }
-     for (int lt = la; lt < lb; ++lt, ++i) {
-      const uint32_t ph = i & 1;
-      // (block 0 landed long before S: this wait orders the converters' row flags before their use here)
-      failed = !tc::warp_wait(&bars->vfull[0], ph, abort) || !tc::warp_wait(&bars->sfull, ph, abort);
-      const bool valid = !failed && ((bars->rowok[i & 3][row >> 3] >> (4 * (row & 7))) & 1u);
-      const uint32_t vmask = valid ? 0xffffffffu : 0u;
-      // Columns that see this row.  Only tiles with rows that some column of the group does not see look at them.
-      uint32_t sees = 0xffffffffu;
-      const bool masked = PACK && (r.j1 - r.j0 < grp.n || lt >= r.na || (lt + 1) * kRowsT > r.least);
-      if (masked) {
-        const int pos = lt < r.na ? lt * kRowsT + row : r.tok0 + (lt - r.na) * kRowsT + row;
-        sees = 0u;
-#pragma unroll 1
-        for (int c = 0; c < 32; ++c) {
-          const int lo = __shfl_sync(0xffffffffu, lt < r.na ? 0 : wlo, c);
-          const int n = __shfl_sync(0xffffffffu, lt < r.na ? ecount : wcount, c);
-          if ((unsigned int)(pos - lo) < (unsigned int)n) sees |= 1u << c;
+      const Run r = grp.run(p, j, lane);
+      j = r.j1;
+      const int la = max(ga - g, 0), lb = min(gb - g, r.n);
+      g += r.n;
+      // packed: the rows that column 32 hsel + lane sees: entries below ecount; window tokens wlo .. wlo + wcount - 1
+      int ecount = 0, wlo = 0, wcount = 0;
+      if (PACK) {
+        const int jc = (32 * hsel + lane) / p.H;
+        const int tj = __shfl_sync(0xffffffffu, grp.t, min(jc, 31)), vj = __shfl_sync(0xffffffffu, grp.vis, min(jc, 31));
+        if (jc >= r.j0 && jc < r.j1) {
+          ecount = vj;
+          wlo = max(0, tj - p.n_win + 1);
+          wcount = tj - wlo + 1;
         }
       }
-      // scores of heads 16 x .. 16 x + 15 of this warp's
-      auto load_scores = [&](int x, uint32_t (&v)[16]) {
-        tc::tmem_ld16(tmem + lanebase + kColS + kHpt * hsel + 16 * x, v);
-        tc::tmem_ld_wait();
-      };
-      // P(i) against the running maxima (PV(i-1), the last reader of the buffer, has completed), zeros in rows that
-      // take no part; returns the largest score (in units of log2) relative to its head's maximum
-      auto write_p = [&]() -> float {
-        float top = neg_inf();
+      for (int lt = la; lt < lb; ++lt, ++i) {
+        const uint32_t ph = i & 1;
+        // (block 0 landed long before S: this wait orders the converters' row flags before their use here)
+        failed = !tc::warp_wait(&bars->vfull[0], ph, abort) || !tc::warp_wait(&bars->sfull, ph, abort);
+        const bool valid = !failed && ((bars->rowok[i & 3][row >> 3] >> (4 * (row & 7))) & 1u);
+        const uint32_t vmask = valid ? 0xffffffffu : 0u;
+        // Columns that see this row.  Only tiles with rows that some column of the group does not see look at them.
+        uint32_t sees = 0xffffffffu;
+        const bool masked = PACK && (r.j1 - r.j0 < grp.n || lt >= r.na || (lt + 1) * kRowsT > r.least);
+        if (masked) {
+          const int pos = lt < r.na ? lt * kRowsT + row : r.tok0 + (lt - r.na) * kRowsT + row;
+          sees = 0u;
+#pragma unroll 1
+          for (int c = 0; c < 32; ++c) {
+            const int lo = __shfl_sync(0xffffffffu, lt < r.na ? 0 : wlo, c);
+            const int n = __shfl_sync(0xffffffffu, lt < r.na ? ecount : wcount, c);
+            if ((unsigned int)(pos - lo) < (unsigned int)n) sees |= 1u << c;
+          }
+        }
+        // A row with an infinity or a NaN that only some columns see must not reach the others as 0 * NaN: it is zeroed
+        // for PV, and the columns that see it get a NaN weight.  Its score is not finite in any column, so one tells
+        // where to look.  (S has been formed: QK^T does not read the row again.)
+        bool nonfinite = false;
+        if (PACK && masked) {
+          if (!failed) tc::fence_after_sync();
+          uint32_t s0 = 0u;
+          if (!failed) {
+            tc::tmem_ld1(tmem + lanebase + kColS + kHpt * hsel, s0);
+            tc::tmem_ld_wait();
+          }
+          const bool odd = valid && (s0 & 0x7f800000u) == 0x7f800000u;
+          if (tc::named_bar_or(1, 32 * kSoft, odd)) {
+            if (odd) {
+#pragma unroll 1
+              for (int w = 0; w < 64; ++w) nonfinite |= any_not_finite(row_part(i, w >> 3)[w & 7]);
+            }
+            tc::named_bar(1, 32 * kSoft);  // (both warps of the quarter have looked)
+            if (nonfinite) {
+#pragma unroll 1
+              for (int w = 32 * hsel; w < 32 * hsel + 32; ++w) row_part(i, w >> 3)[w & 7] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+        // scores of heads 16 x .. 16 x + 15 of this warp's
+        auto load_scores = [&](int x, uint32_t (&v)[16]) {
+          tc::tmem_ld16(tmem + lanebase + kColS + kHpt * hsel + 16 * x, v);
+          tc::tmem_ld_wait();
+        };
+        // P(i) against the running maxima (PV(i-1), the last reader of the buffer, has completed), zeros in rows that
+        // take no part; returns the largest score (in units of log2) relative to its head's maximum
+        auto write_p = [&]() -> float {
+          float top = neg_inf();
 #pragma unroll
+          for (int x = 0; x < kHpt / 16; ++x) {
+            uint32_t v[16], w[8];
+            load_scores(x, v);
+            float sv[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float4 m4 = *reinterpret_cast<const float4*>(bars->nref + kHpt * hsel + 16 * x + 4 * c);
+              sv[4 * c] = fmaf(__uint_as_float(v[4 * c]), scale_log2, m4.x);
+              sv[4 * c + 1] = fmaf(__uint_as_float(v[4 * c + 1]), scale_log2, m4.y);
+              sv[4 * c + 2] = fmaf(__uint_as_float(v[4 * c + 2]), scale_log2, m4.z);
+              sv[4 * c + 3] = fmaf(__uint_as_float(v[4 * c + 3]), scale_log2, m4.w);
+            }
+            if (PACK && masked) {
+#pragma unroll
+              for (int h = 0; h < 16; ++h)
+                sv[h] = (sees >> (16 * x + h)) & 1u ? (nonfinite ? __uint_as_float(0x7fffffffu) : sv[h]) : neg_inf();
+            }
+#pragma unroll
+            for (int h = 0; h < 16; h += 2) top = fmaxf(top, fmaxf(sv[h], sv[h + 1]));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(fast_exp2(sv[2 * k]), fast_exp2(sv[2 * k + 1])) & vmask;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              const int c = (kHpt / 8) * hsel + 2 * x + cc;  // 16-byte unit of the row: columns 8c .. 8c+7
+              *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
+                  make_uint4(w[4 * cc], w[4 * cc + 1], w[4 * cc + 2], w[4 * cc + 3]);
+            }
+          }
+          return valid ? top : neg_inf();
+        };
+        if (!failed) tc::fence_after_sync();
+        const float top = i == 0 ? INFINITY : write_p();  // (the first tile sets the maxima in any case)
+        // One vote for "no score lies above its head's running maximum + 2^8 and nobody failed", the usual case: P
+        // stands.  Otherwise new maxima, rescaled accumulators, and P again.
+        if (tc::named_bar_or(1, 32 * kSoft, top > kRescaleLog2 || failed || *abort)) {
+          if (tc::named_bar_or(1, 32 * kSoft, failed || *abort)) { failed = true; break; }
+#pragma unroll 1
+          for (int x = 0; x < kHpt / 16; ++x) {
+            uint32_t v[16];
+            load_scores(x, v);
+            const uint32_t ok = (sees & vmask) >> (16 * x);
+            float m = 0.f;
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+              const float y = warp_max((ok >> h) & 1u ? __uint_as_float(v[h]) * scale_log2 : neg_inf());
+              if (lane == h) m = y;
+            }
+            if (lane < 16) bars->red[quarter][kHpt * hsel + 16 * x + lane] = m;
+          }
+          tc::named_bar(1, 32 * kSoft);
+          if (st < kHT) {
+            const float mt = fmaxf(fmaxf(bars->red[0][st], bars->red[1][st]), fmaxf(bars->red[2][st], bars->red[3][st]));
+            const float mo = -bars->nref[st];
+            const bool grow = mt > mo + kRescaleLog2;
+            bars->alpha[st] = grow ? fast_exp2(mo - mt) : 1.f;
+            if (grow) bars->nref[st] = -mt;
+          }
+          tc::named_bar(1, 32 * kSoft);
+          lw *= bars->alpha[kHpt * hsel + lane];
+          if (i > 0) {
+            // O^T holds the sums up to tile i-1 (PV(i-1) was issued before QK(i), whose commit has arrived)
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int part = 0; part < kBlocks * (kHpt / 16); ++part) {
+              const int hh = kHpt * hsel + 16 * (part & 1);
+              const uint32_t ta = tmem + lanebase + kColO + (part >> 1) * kHT + hh;
+              uint32_t v[16];
+              tc::tmem_ld16(ta, v);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < 16; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * bars->alpha[hh + h]);
+              tc::tmem_st16(ta, v);
+            }
+            tc::tmem_st_wait();
+          }
+          write_p();
+        }
+        tc::fence_before_sync();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->pfull);
+        // the row sums of exactly what PV multiplies, read back from this thread's own row
+#pragma unroll 1
         for (int x = 0; x < kHpt / 16; ++x) {
-          uint32_t v[16], w[8];
-          load_scores(x, v);
           float sv[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float4 m4 = *reinterpret_cast<const float4*>(bars->nref + kHpt * hsel + 16 * x + 4 * c);
-            sv[4 * c] = fmaf(__uint_as_float(v[4 * c]), scale_log2, m4.x);
-            sv[4 * c + 1] = fmaf(__uint_as_float(v[4 * c + 1]), scale_log2, m4.y);
-            sv[4 * c + 2] = fmaf(__uint_as_float(v[4 * c + 2]), scale_log2, m4.z);
-            sv[4 * c + 3] = fmaf(__uint_as_float(v[4 * c + 3]), scale_log2, m4.w);
-          }
-          if (PACK && masked) {
-#pragma unroll
-            for (int h = 0; h < 16; ++h) sv[h] = (sees >> (16 * x + h)) & 1u ? sv[h] : neg_inf();
-          }
-#pragma unroll
-          for (int h = 0; h < 16; h += 2) top = fmaxf(top, fmaxf(sv[h], sv[h + 1]));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(fast_exp2(sv[2 * k]), fast_exp2(sv[2 * k + 1])) & vmask;
-#pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
-            const int c = (kHpt / 8) * hsel + 2 * x + cc;  // 16-byte unit of the row: columns 8c .. 8c+7
-            *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
-                make_uint4(w[4 * cc], w[4 * cc + 1], w[4 * cc + 2], w[4 * cc + 3]);
-          }
-        }
-        return valid ? top : neg_inf();
-      };
-      if (!failed) tc::fence_after_sync();
-      const float top = i == 0 ? INFINITY : write_p();  // (the first tile sets the maxima in any case)
-      // One vote for "no score lies above its head's running maximum + 2^8 and nobody failed", the usual case: P
-      // stands.  Otherwise new maxima, rescaled accumulators, and P again.
-      if (tc::named_bar_or(1, 32 * kSoft, top > kRescaleLog2 || failed || *abort)) {
-        if (tc::named_bar_or(1, 32 * kSoft, failed || *abort)) { failed = true; break; }
-#pragma unroll 1
-        for (int x = 0; x < kHpt / 16; ++x) {
-          uint32_t v[16];
-          load_scores(x, v);
-          const uint32_t ok = (sees & vmask) >> (16 * x);
-          float m = 0.f;
+            const int c = (kHpt / 8) * hsel + 2 * x + cc;
+            float f[8];
+            unpack8(*reinterpret_cast<const uint4*>(prow + ((c ^ (row & 7)) << 4)), f);
 #pragma unroll
-          for (int h = 0; h < 16; ++h) {
-            const float y = warp_max((ok >> h) & 1u ? __uint_as_float(v[h]) * scale_log2 : neg_inf());
-            if (lane == h) m = y;
+            for (int h = 0; h < 8; ++h) sv[8 * cc + h] = f[h];
           }
-          if (lane < 16) bars->red[quarter][kHpt * hsel + 16 * x + lane] = m;
+          const float t = warp_sum16(sv, lane);
+          if ((lane >> 4) == x) lw += t;
         }
-        tc::named_bar(1, 32 * kSoft);
-        if (st < kHT) {
-          const float mt = fmaxf(fmaxf(bars->red[0][st], bars->red[1][st]), fmaxf(bars->red[2][st], bars->red[3][st]));
-          const float mo = -bars->nref[st];
-          const bool grow = mt > mo + kRescaleLog2;
-          bars->alpha[st] = grow ? fast_exp2(mo - mt) : 1.f;
-          if (grow) bars->nref[st] = -mt;
-        }
-        tc::named_bar(1, 32 * kSoft);
-        lw *= bars->alpha[kHpt * hsel + lane];
-        if (i > 0) {
-          // O^T holds the sums up to tile i-1 (PV(i-1) was issued before QK(i), whose commit has arrived)
-          tc::fence_after_sync();
-#pragma unroll 1
-          for (int part = 0; part < kBlocks * (kHpt / 16); ++part) {
-            const int hh = kHpt * hsel + 16 * (part & 1);
-            const uint32_t ta = tmem + lanebase + kColO + (part >> 1) * kHT + hh;
-            uint32_t v[16];
-            tc::tmem_ld16(ta, v);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int h = 0; h < 16; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * bars->alpha[hh + h]);
-            tc::tmem_st16(ta, v);
-          }
-          tc::tmem_st_wait();
-        }
-        write_p();
       }
-      tc::fence_before_sync();
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->pfull);
-      // the row sums of exactly what PV multiplies, read back from this thread's own row
-#pragma unroll 1
-      for (int x = 0; x < kHpt / 16; ++x) {
-        float sv[16];
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          const int c = (kHpt / 8) * hsel + 2 * x + cc;
-          float f[8];
-          unpack8(*reinterpret_cast<const uint4*>(prow + ((c ^ (row & 7)) << 4)), f);
-#pragma unroll
-          for (int h = 0; h < 8; ++h) sv[8 * cc + h] = f[h];
-        }
-        const float t = warp_sum16(sv, lane);
-        if ((lane >> 4) == x) lw += t;
-      }
-     }
     }
     // ---- epilogue: O^T (channels x columns) and the row sums ----
     bars->red[quarter][kHpt * hsel + lane] = lw;
@@ -641,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
         // a sink logit joins the denominator here (base-2, against the running maximum), for partial states in the
         // combine
         if (p.sink != nullptr && h0 + st < p.H && l > 0.f) l += fast_exp2(p.sink[h0 + st] * kLog2e + bars->nref[st]);
-        bars->alpha[st] = l > 0.f ? __fdividef(1.f, l) : 0.f;
+        bars->alpha[st] = l == 0.f ? 0.f : __fdividef(1.f, l);  // (NaN stays)
       }
     }
     if (all_done(!failed)) {
@@ -668,138 +706,138 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     bool okw = true;
     int i = 0, g = 0;
     for (int j = 0; j < grp.n && okw;) {
-    const Run r = grp.run(p, j, lane);
-    j = r.j1;
-    const int la = max(ga - g, 0), lb = min(gb - g, r.n), le = min(lb, r.na);
-    g += r.n;
-    // Entry of this thread's row of the run's tile lt (-1: none), among those of this CTA.
-    auto entry_of = [&](int lt) -> int {
-      const int u = lt * kRowsT + row;
-      if (lt >= le || u >= r.entries) return -1;
-      return grp.idx ? grp.idx[u] : u;
-    };
-    // The block that entry e lies in (paged), loaded but not looked at yet, and its cache row from it.
-    auto block_of = [&](int e) -> int {
-      if (!p.kv.bt || e < 0 || e >= p.N) return 0;
-      const unsigned int j = div_by(e, p.kv.div);
-      return j < p.kv.bt_stride ? p.kv.bt[r.req * p.kv.bt_stride + j] : -1;
-    };
-    auto resolve = [&](int lt, int e, int blk) -> int {
-      if (p.check && sub == 0 && grp.idx && lt < le && lt * kRowsT + row < r.entries) {
-        const unsigned int k = entry_check(e, grp.t, p.rate, p.N);
-        if (k) atomicOr(&g_mqa_fp4_error, k << 1);
-      }
-      if (e < 0 || e >= p.N) return -1;
-      long long x = p.kv.bt ? (blk < 0 ? -1ll : (long long)blk * p.kv.rpb + (e - (int)(div_by(e, p.kv.div) * p.kv.div.d)))
-                            : (e < p.kv.seq_rows ? r.req * p.kv.seq_rows + e : -1ll);
-      if (x >= p.kv.n_rows) x = -1;
-      if (p.check && x < 0) atomicOr(&g_mqa_fp4_error, kIdxBlock << 1);
-      return (int)x;
-    };
-    // The codes of this thread's group of block b of cache row x, in the order of its stores (halves swapped in the
-    // second chunk).
-    auto fetch = [&](int x, int b) -> uint4 {
-      const uint4 v = x >= 0 && 4 * b + sub < n_groups ? *reinterpret_cast<const uint4*>(codes + x * p.kv.ld_codes + b * 64)
-                                                       : make_uint4(0u, 0u, 0u, 0u);
-      return chunk ? make_uint4(v.z, v.w, v.x, v.y) : v;
-    };
-    auto fetch_scales = [&](int x) -> uint4 {
-      return x >= 0 ? *reinterpret_cast<const uint4*>(scales + x * p.kv.ld_scales) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    // This thread's row of chunk c of tile i.
-    auto row_of = [&](int i, int c) -> unsigned char* { return kv + c * kKvChunk + (c == 7 && (i & 1) ? kR2Delta : 0u); };
-    // Copies a quarter of a 128-byte row of chunk c (units 2 sub and 2 sub + 1); zeros where there is none.
-    auto copy_row = [&](int i, int c, const bf16* src, bool ok) {
-      const uint32_t dst = tc::smem_u32(row_of(i, c));
-#pragma unroll
-      for (uint32_t w = 0; w < 2; ++w)
-        tc::cp_async16(dst + (((2 * sub + w) ^ sw) << 4), src + (2 * sub + w) * 8, ok ? 16 : 0);
-    };
-    // The 64 rotary channels of cache row x, into the last chunk of tile i.
-    auto copy_rope = [&](int i, int x) {
-      copy_row(i, 7, p.kv.rope + (x >= 0 ? x * p.kv.ld_rope : 0ll), x >= 0);
-      tc::cp_async_commit();
-    };
-    // An entry's index, its block and its row are dependent loads, each given a tile's time: x is the cache row of the
-    // tile being converted, e1 and b1 entry and block of the next one, e2 the entry of the one after.
-    const int e0 = entry_of(la);
-    int e1 = entry_of(la + 1), e2 = entry_of(la + 2);
-    int x = resolve(la, e0, block_of(e0));
-    int b1 = block_of(e1);
-    if (rope64 && la < le) copy_rope(i, x);  // (PV of tile i-2 has released this buffer)
-    // Widen this thread's group of block b (one that is not held in 4 bits: its codes are zeros).
-    auto widen = [&](int b, const uint4& v, uint32_t scale_word, uint4 (&o)[4]) {
-      e2m1x32_to_bf16(v, (scale_word >> (8 * sub)) & 255u, o);
-    };
-    // Store a widened group of block b and signal the block.
-    auto put = [&](int i, int b, const uint4 (&o)[4]) {
-      const int g = 4 * b + sub;
-      unsigned char* d = row_of(i, 2 * b + chunk);
-      if (g < n_groups) {
-#pragma unroll
-        for (uint32_t w = 0; w < 4; ++w) *reinterpret_cast<uint4*>(d + (((unit0 ^ w) ^ sw) << 4)) = o[w];
-      } else if (!rope64) {  // other numbers of rotary channels: copied here
-        const bf16* src = p.kv.rope + (x >= 0 ? x * p.kv.ld_rope + (g - n_groups) * 32 : 0ll);
-#pragma unroll 1
-        for (uint32_t w = 0; w < 4; ++w)
-          tc::cp_async16(tc::smem_u32(d) + (((4 * (sub & 1) + w) ^ sw) << 4), src + w * 8, x >= 0 ? 16 : 0);
-        tc::cp_async_commit();
-      }
-      if (b == kBlocks - 1 || !rope64) tc::cp_async_wait<0>();  // (64 rotary channels: under way since the last tile)
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->vfull[b]);
-    };
-    int lt = la;
-    for (; okw && lt < le; ++lt, ++i) {
-      const uint32_t ph = i & 1;
-      const uint32_t mask = __ballot_sync(0xffffffffu, x >= 0);
-      if (lane == 0) bars->rowok[i & 3][cw] = mask;
-      uint4 oa[4], ob[4], oc[4];
-      const uint4 sc = fetch_scales(x);
-      const uint4 v0 = fetch(x, 0), v1 = fetch(x, 1), v2 = fetch(x, 2), v3 = fetch(x, 3);
-      widen(0, v0, sc.x, oa);
-      widen(1, v1, sc.y, ob);
-      widen(2, v2, sc.z, oc);
-      if (!(okw = tc::warp_wait(&bars->vempty[0], ph ^ 1, abort))) break;
-      put(i, 0, oa);
-      widen(3, v3, sc.w, oa);
-      if (!(okw = tc::warp_wait(&bars->vempty[kBlocks - 1], ph ^ 1, abort))) break;
-      put(i, 1, ob);
-      put(i, 2, oc);
-      put(i, 3, oa);
-      // PV of tile i-1 has released its buffer of the last chunk: it takes tile i+1's
-      x = resolve(lt + 1, e1, b1);
-      if (rope64 && lt + 1 < le) copy_rope(i + 1, x);
-      e1 = e2;
-      b1 = block_of(e1);
-      e2 = entry_of(lt + 3);
-    }
-    for (; okw && lt < lb; ++lt, ++i) {  // window rows
-      const uint32_t ph = i & 1;
-      const int w = (lt - r.na) * kRowsT + row;
-      const bool valid = w < r.window;
-      const uint32_t mask = __ballot_sync(0xffffffffu, valid);
-      if (lane == 0) bars->rowok[i & 3][cw] = mask;
-      const bf16* src = valid ? p.win + r.req * p.win_seq_stride + (long long)((r.tok0 + w) % p.win_rows) * kC : p.win;
-#pragma unroll 1
-      for (int b = 0; b < kBlocks; ++b) {
-        if (!tc::warp_wait(&bars->vempty[b], ph ^ 1, abort)) { okw = false; break; }
-        copy_row(i, 2 * b, src + b * 128, valid);
-        copy_row(i, 2 * b + 1, src + b * 128 + 64, valid);
-        tc::cp_async_commit();
-        if (b > 0) {
-          tc::cp_async_wait<1>();
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bars->vfull[b - 1]);
+      const Run r = grp.run(p, j, lane);
+      j = r.j1;
+      const int la = max(ga - g, 0), lb = min(gb - g, r.n), le = min(lb, r.na);
+      g += r.n;
+      // Entry of this thread's row of the run's tile lt (-1: none), among those of this CTA.
+      auto entry_of = [&](int lt) -> int {
+        const int u = lt * kRowsT + row;
+        if (lt >= le || u >= r.entries) return -1;
+        return grp.idx ? grp.idx[u] : u;
+      };
+      // The block that entry e lies in (paged), loaded but not looked at yet, and its cache row from it.
+      auto block_of = [&](int e) -> int {
+        if (!p.kv.bt || e < 0 || e >= p.N) return 0;
+        const unsigned int j = div_by(e, p.kv.div);
+        return j < p.kv.bt_stride ? p.kv.bt[r.req * p.kv.bt_stride + j] : -1;
+      };
+      auto resolve = [&](int lt, int e, int blk) -> int {
+        if (p.check && sub == 0 && grp.idx && lt < le && lt * kRowsT + row < r.entries) {
+          const unsigned int k = entry_check(e, grp.t, p.rate, p.N);
+          if (k) atomicOr(&g_mqa_fp4_error, k << 1);
         }
+        if (e < 0 || e >= p.N) return -1;
+        long long x = p.kv.bt ? (blk < 0 ? -1ll : (long long)blk * p.kv.rpb + (e - (int)(div_by(e, p.kv.div) * p.kv.div.d)))
+                              : (e < p.kv.seq_rows ? r.req * p.kv.seq_rows + e : -1ll);
+        if (x >= p.kv.n_rows) x = -1;
+        if (p.check && x < 0) atomicOr(&g_mqa_fp4_error, kIdxBlock << 1);
+        return (int)x;
+      };
+      // The codes of this thread's group of block b of cache row x, in the order of its stores (halves swapped in the
+      // second chunk).
+      auto fetch = [&](int x, int b) -> uint4 {
+        const uint4 v = x >= 0 && 4 * b + sub < n_groups ? *reinterpret_cast<const uint4*>(codes + x * p.kv.ld_codes + b * 64)
+                                                         : make_uint4(0u, 0u, 0u, 0u);
+        return chunk ? make_uint4(v.z, v.w, v.x, v.y) : v;
+      };
+      auto fetch_scales = [&](int x) -> uint4 {
+        return x >= 0 ? *reinterpret_cast<const uint4*>(scales + x * p.kv.ld_scales) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      // This thread's row of chunk c of tile i.
+      auto row_of = [&](int i, int c) -> unsigned char* { return kv + c * kKvChunk + (c == 7 && (i & 1) ? kR2Delta : 0u); };
+      // Copies a quarter of a 128-byte row of chunk c (units 2 sub and 2 sub + 1); zeros where there is none.
+      auto copy_row = [&](int i, int c, const bf16* src, bool ok) {
+        const uint32_t dst = tc::smem_u32(row_of(i, c));
+#pragma unroll
+        for (uint32_t w = 0; w < 2; ++w)
+          tc::cp_async16(dst + (((2 * sub + w) ^ sw) << 4), src + (2 * sub + w) * 8, ok ? 16 : 0);
+      };
+      // The 64 rotary channels of cache row x, into the last chunk of tile i.
+      auto copy_rope = [&](int i, int x) {
+        copy_row(i, 7, p.kv.rope + (x >= 0 ? x * p.kv.ld_rope : 0ll), x >= 0);
+        tc::cp_async_commit();
+      };
+      // An entry's index, its block and its row are dependent loads, each given a tile's time: x is the cache row of the
+      // tile being converted, e1 and b1 entry and block of the next one, e2 the entry of the one after.
+      const int e0 = entry_of(la);
+      int e1 = entry_of(la + 1), e2 = entry_of(la + 2);
+      int x = resolve(la, e0, block_of(e0));
+      int b1 = block_of(e1);
+      if (rope64 && la < le) copy_rope(i, x);  // (PV of tile i-2 has released this buffer)
+      // Widen this thread's group of block b (one that is not held in 4 bits: its codes are zeros).
+      auto widen = [&](int b, const uint4& v, uint32_t scale_word, uint4 (&o)[4]) {
+        e2m1x32_to_bf16(v, (scale_word >> (8 * sub)) & 255u, o);
+      };
+      // Store a widened group of block b and signal the block.
+      auto put = [&](int i, int b, const uint4 (&o)[4]) {
+        const int g = 4 * b + sub;
+        unsigned char* d = row_of(i, 2 * b + chunk);
+        if (g < n_groups) {
+#pragma unroll
+          for (uint32_t w = 0; w < 4; ++w) *reinterpret_cast<uint4*>(d + (((unit0 ^ w) ^ sw) << 4)) = o[w];
+        } else if (!rope64) {  // other numbers of rotary channels: copied here
+          const bf16* src = p.kv.rope + (x >= 0 ? x * p.kv.ld_rope + (g - n_groups) * 32 : 0ll);
+#pragma unroll 1
+          for (uint32_t w = 0; w < 4; ++w)
+            tc::cp_async16(tc::smem_u32(d) + (((4 * (sub & 1) + w) ^ sw) << 4), src + w * 8, x >= 0 ? 16 : 0);
+          tc::cp_async_commit();
+        }
+        if (b == kBlocks - 1 || !rope64) tc::cp_async_wait<0>();  // (64 rotary channels: under way since the last tile)
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->vfull[b]);
+      };
+      int lt = la;
+      for (; okw && lt < le; ++lt, ++i) {
+        const uint32_t ph = i & 1;
+        const uint32_t mask = __ballot_sync(0xffffffffu, x >= 0);
+        if (lane == 0) bars->rowok[i & 3][cw] = mask;
+        uint4 oa[4], ob[4], oc[4];
+        const uint4 sc = fetch_scales(x);
+        const uint4 v0 = fetch(x, 0), v1 = fetch(x, 1), v2 = fetch(x, 2), v3 = fetch(x, 3);
+        widen(0, v0, sc.x, oa);
+        widen(1, v1, sc.y, ob);
+        widen(2, v2, sc.z, oc);
+        if (!(okw = tc::warp_wait(&bars->vempty[0], ph ^ 1, abort))) break;
+        put(i, 0, oa);
+        widen(3, v3, sc.w, oa);
+        if (!(okw = tc::warp_wait(&bars->vempty[kBlocks - 1], ph ^ 1, abort))) break;
+        put(i, 1, ob);
+        put(i, 2, oc);
+        put(i, 3, oa);
+        // PV of tile i-1 has released its buffer of the last chunk: it takes tile i+1's
+        x = resolve(lt + 1, e1, b1);
+        if (rope64 && lt + 1 < le) copy_rope(i + 1, x);
+        e1 = e2;
+        b1 = block_of(e1);
+        e2 = entry_of(lt + 3);
       }
-      tc::cp_async_wait<0>();
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (okw && lane == 0) tc::mbar_arrive(&bars->vfull[kBlocks - 1]);
-    }
+      for (; okw && lt < lb; ++lt, ++i) {  // window rows
+        const uint32_t ph = i & 1;
+        const int w = (lt - r.na) * kRowsT + row;
+        const bool valid = w < r.window;
+        const uint32_t mask = __ballot_sync(0xffffffffu, valid);
+        if (lane == 0) bars->rowok[i & 3][cw] = mask;
+        const bf16* src = valid ? p.win + r.req * p.win_seq_stride + (long long)((r.tok0 + w) % p.win_rows) * kC : p.win;
+#pragma unroll 1
+        for (int b = 0; b < kBlocks; ++b) {
+          if (!tc::warp_wait(&bars->vempty[b], ph ^ 1, abort)) { okw = false; break; }
+          copy_row(i, 2 * b, src + b * 128, valid);
+          copy_row(i, 2 * b + 1, src + b * 128 + 64, valid);
+          tc::cp_async_commit();
+          if (b > 0) {
+            tc::cp_async_wait<1>();
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars->vfull[b - 1]);
+          }
+        }
+        tc::cp_async_wait<0>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (okw && lane == 0) tc::mbar_arrive(&bars->vfull[kBlocks - 1]);
+      }
     }
     tc::cp_async_wait<0>();
     if (all_done(okw)) {
@@ -839,8 +877,10 @@ MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms) {
     const int smax = (int)min((long long)min(tiles, 1024), max(1ll, 2ll * num_sms / ctas1));
     int best = 1;
     long long best_cost = -1;
-    for (int s = 1; s <= smax; ++s) {
-      const int tpc = (tiles + s - 1) / s, eff = (tiles + tpc - 1) / tpc;
+    // the fewest splits of each number of tiles per CTA
+    for (int s = 1, tpc; s <= smax; s = tpc > 1 ? (tiles + tpc - 2) / (tpc - 1) : smax + 1) {
+      tpc = (tiles + s - 1) / s;
+      const int eff = (tiles + tpc - 1) / tpc;
       const long long waves = (ctas1 * eff + num_sms - 1) / num_sms;
       const long long cost = waves * (tpc * 4 + 6) + (eff > 1 ? 4 : 0);
       if (best_cost < 0 || cost < best_cost) { best_cost = cost; best = eff; }

@@ -220,6 +220,30 @@ def test_many_queries_unsplit():
     sub.check(got[keep], pos[keep], q_req=req[keep])
 
 
+@pytest.mark.parametrize("H", [4, 16, 64])
+@pytest.mark.parametrize("where", ["entry", "window"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_nonfinite_rows_that_earlier_queries_do_not_see(H, where, value):
+    """Queries of one chunk: a row that is not finite reaches the queries that see it and no other."""
+    s = Setup(H=H, B=1, N=300, nq=4, seed=H)
+    pos = np.array([601, 602, 603, 604])  # rate 4: 150 entries are visible to the first two, 151 to the others
+    first, clean = 2, s.win.clone()
+    if where == "entry":
+        s.k.t["rope"].view(-1, s.k.t["rope"].shape[-1])[s.k.row(0, 150), 5] = value
+    else:
+        s.win[0, 603 % s.W, 17] = value
+    out = s.call(pos, q_req=[0] * 4)
+    s.win = clean
+    got = to64(out)
+    assert np.isfinite(got[:first]).all()
+    for i in range(first):
+        check_query(got[i], to64(s.q[i]), s.rows(i, int(pos[i]), 0, 4, None), s.cfg.scale, what=f"query {i}")
+    if np.isnan(value):
+        assert np.isnan(got[first:]).all()
+    else:
+        assert (~np.isfinite(got[first:])).any(axis=(1, 2)).all()
+
+
 @pytest.mark.parametrize("c,rope,H", [(64, 0, 4), (64, 32, 4), (128, 64, 8), (256, 0, 64), (480, 64, 3), (512, 0, 64),
                                       (512, 256, 64)])
 def test_other_widths(c, rope, H):
