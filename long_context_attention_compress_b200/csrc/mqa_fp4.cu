@@ -189,7 +189,7 @@ constexpr uint32_t kOffQ = 0, kOffKv = kQBytes, kOffP = kOffKv + kKvBytes, kOffR
 constexpr uint32_t kOffBars = kOffR2 + kKvChunk;
 constexpr uint32_t kR2Delta = kOffR2 - (kOffKv + 7 * kKvChunk);  // second buffer of the last chunk, after the first
 constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
-constexpr float kRescaleLog2 = 8.f;
+constexpr float kRescaleLog2 = 20.f;
 constexpr float kNoMax = -1e30f;                      // running maximum of a head without a score yet
 constexpr int kHpt = kHT * 4 / kSoft;                // heads per softmax thread (32)
 constexpr int kOutLd = kC + 8;                       // staged output row (bf16), padded against bank conflicts
@@ -600,8 +600,26 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
           return valid ? top : neg_inf();
         };
         if (!failed) tc::fence_after_sync();
-        const float top = i == 0 ? INFINITY : write_p();  // (the first tile sets the maxima in any case)
-        // One vote for "no score lies above its head's running maximum + 2^8 and nobody failed", the usual case: P
+        if (i == 0) {
+          // The first row's scores as the first references: none exceeds its column's maximum.
+          if (quarter == 0) {
+#pragma unroll 1
+            for (int x = 0; x < kHpt / 16; ++x) {
+              uint32_t v[16];
+              load_scores(x, v);
+              if (lane == 0 && valid) {
+#pragma unroll
+                for (int h = 0; h < 16; ++h) {
+                  const float m = __uint_as_float(v[h]) * scale_log2;
+                  if (((sees >> (16 * x + h)) & 1u) && fabsf(m) < -kNoMax) bars->nref[kHpt * hsel + 16 * x + h] = -m;
+                }
+              }
+            }
+          }
+          tc::named_bar(1, 32 * kSoft);
+        }
+        const float top = write_p();
+        // One vote for "no score lies above its head's running reference + 20 and nobody failed", the usual case: P
         // stands.  Otherwise new maxima, rescaled accumulators, and P again.
         if (tc::named_bar_or(1, 32 * kSoft, top > kRescaleLog2 || failed || *abort)) {
           if (tc::named_bar_or(1, 32 * kSoft, failed || *abort)) { failed = true; break; }
