@@ -11,7 +11,7 @@
 // float64 value: a quantised code must not depend on which side of a midpoint an f32 normalisation falls.  Sum of
 // squares and rotation are f64; the other channels are formed in f32, 8 ulps too low and too high (f32 is within 4),
 // and redone in f64 only where the two round apart.  The codes are those of the stored-form definitions bit for bit: FP4 scaling is
-// exact and the conversion rounds to nearest even; an f32 quotient within 4 ulps of an E4M3 midpoint, or in E4M3's
+// exact and the conversion rounds to nearest even; an f32 quotient (by the reciprocal, within 2 ulps) within 4 of an E4M3 midpoint, or in E4M3's
 // subnormal range, is decided on the f64 quotient.
 //
 // The angle is formed in turns from theta / 2 pi in two f64 words (a table made on the host) with an error-free product,
@@ -19,6 +19,8 @@
 //
 // kv_gather_kernel.  The bf16 values of rows.  Each row is a chain of dependent loads (index, block table, row): a block
 // resolves 32 rows at a time, one a thread, while its warps move the 32 before, four rows in flight per warp.
+
+#include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cmath>
@@ -68,15 +70,26 @@ __device__ __forceinline__ uint32_t e2m1x8_encode(const float* y) {
 // straight line, for the elements that need it.
 __device__ __forceinline__ bool e4m3_doubtful(float q) {
   const int low = (int)(__float_as_uint(q) & 0xfffffu) - 0x80000;
-  return !(fabsf(q) >= 0.015625f) || (low >= -4 && low <= 4);
+  return fabsf(q) < 0.015625f || (low >= -4 && low <= 4);  // (a NaN is converted to the code of NaN)
 }
-__device__ __noinline__ uint32_t e4m3_decide(float y, float sc) { return e4m3_encode((double)y / (double)sc); }
+// Rounded in f64 to a multiple of E4M3's spacing at its magnitude, ties to even, by adding and taking off 2^52 of them;
+// what is left is a code's value (or past the largest one).
+__device__ __noinline__ uint32_t e4m3_decide(float y, float sc) {
+  const double q = (double)y / (double)sc, a = fabs(q);
+  const int e = max((__double2hiint(a) >> 20) - 1023, -6);
+  const double big = __hiloint2double((e - 3 + 52 + 1023) << 20, 0);
+  const float r = (float)copysign((a + big) - big, q);
+  uint16_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(h) : "f"(r));
+  return r != 0.f ? h & 255u : q < 0.0 ? 128u : 0u;
+}
 __device__ __forceinline__ uint2 e4m3x8_encode(const float* y, float sc) {
   uint32_t w[4];
-  uint32_t doubt = 0;
+  uint32_t doubt = sc < 0x1p-100f ? 255u : 0u;  // (whose reciprocal may overflow)
+  const float r_sc = 1.f / sc;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const float q0 = y[2 * t] / sc, q1 = y[2 * t + 1] / sc;
+    const float q0 = y[2 * t] * r_sc, q1 = y[2 * t + 1] * r_sc;  // within 2 ulps of the quotient
     uint16_t h;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(q1), "f"(q0));
     w[t] = h;
@@ -108,13 +121,15 @@ constexpr int append_blocks(int form, bool xf) { return xf ? 6 : form == HCA_KV_
 // channels that are only converted (the indexer's keys), else 32.
 template <bool F32, int FORM, bool XF, int LANES>
 __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
-    kv_append_kernel(KvAppend a, KvCache k, int rows_per_group, const __grid_constant__ Turns turns) {
+    kv_append_kernel(KvAppend a, KvCache k, int base_rows, int one_more, const __grid_constant__ Turns turns) {
   constexpr int kU = LANES == 32 ? kKvChunks : 1;  // chunks per lane
   __shared__ double2 s_cs[XF ? kKvWarps : 1][kKvMaxPairs];  // cosine and sine of each pair at the warp's position
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, sub = lane & (LANES - 1);
   const unsigned int all = LANES == 32 ? 0xffffffffu : 0xffffu << (lane & 16);  // this row's lanes
-  const int r0 = ((blockIdx.x * kKvWarps + wib) * (32 / LANES) + lane / LANES) * rows_per_group;
-  const int r1 = min(a.n_rows, r0 + rows_per_group);
+  // base_rows rows a group of lanes; the first one_more groups take one more
+  const int grp = (blockIdx.x * kKvWarps + wib) * (32 / LANES) + lane / LANES;
+  const int r0 = grp * base_rows + min(grp, one_more);
+  const int r1 = min(a.n_rows, r0 + base_rows + (grp < one_more ? 1 : 0));
   if (r0 >= r1) return;
   const int nch = k.c >> 3;
   const int rope0 = k.c - k.rope_dims;
@@ -307,11 +322,15 @@ __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
   }
 }
 
-// E4M3 byte times an f32 scale (one rounding, in the product): the magnitude's bits, seen as an f32 2^120 too
-// small, are exact for subnormal codes too.
-__device__ __forceinline__ float e4m3_scaled(uint32_t b, float sc) {
-  const float mag = __uint_as_float((b & 0x7fu) << 20) * 1.329227995784916e36f;  // 2^120
-  return ((b & 0x80u) ? -mag : mag) * sc;
+// Two E4M3 codes times an f32 scale, in bf16: both are exact in f16 and f32, so the rounding is the product's to f32
+// and its to bf16.
+__device__ __forceinline__ uint32_t e4m3x2_scaled(uint32_t two, float sc) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(two));
+  __half2 v;
+  memcpy(&v, &h, 4);
+  const float2 f = __half22float2(v);
+  return pack_bf16x2(f.x * sc, f.y * sc);
 }
 
 // Loads that are made or not (zeros) without a branch, so that a batch of them is under way at once.
@@ -426,10 +445,8 @@ __global__ void __launch_bounds__(256, kGatherResident) kv_gather_kernel(KvCache
             if constexpr (FORM == HCA_KV_FP8) {
               const float s = __uint_as_float(sc[u][r]);
               const uint32_t lo = raw[u][r].x, hi = raw[u][r].y;
-              w.x = pack_bf16x2(e4m3_scaled(lo, s), e4m3_scaled(lo >> 8, s));
-              w.y = pack_bf16x2(e4m3_scaled(lo >> 16, s), e4m3_scaled(lo >> 24, s));
-              w.z = pack_bf16x2(e4m3_scaled(hi, s), e4m3_scaled(hi >> 8, s));
-              w.w = pack_bf16x2(e4m3_scaled(hi >> 16, s), e4m3_scaled(hi >> 24, s));
+              w = make_uint4(e4m3x2_scaled(lo, s), e4m3x2_scaled(lo >> 16, s), e4m3x2_scaled(hi, s),
+                             e4m3x2_scaled(hi >> 16, s));
             } else if constexpr (FORM == HCA_KV_FP4) {
               w = e2m1x8_times(raw[u][r].x, e8m0_bf16x2(sc[u][r]));
             }
@@ -468,12 +485,12 @@ static void append_rows(const KvAppend& a, const KvCache& k, cudaStream_t stream
   // one row a group of lanes until the machine is full (the resident warps of the launch bounds), then contiguous runs
   const int groups = !xf && k.c <= 128 ? 2 : 1;  // per warp
   const int max_groups = device_sm_count() * kKvWarps * append_blocks(FORM, xf) * groups;
-  const int per = (a.n_rows + max_groups - 1) / max_groups;
-  const int blocks = (a.n_rows + per * kKvWarps * groups - 1) / (per * kKvWarps * groups);
+  const int used = std::min(a.n_rows, max_groups), per = a.n_rows / used, more = a.n_rows - per * used;
+  const int blocks = (used + kKvWarps * groups - 1) / (kKvWarps * groups);
   const dim3 block(32 * kKvWarps);
-  if (xf) kv_append_kernel<F32, FORM, true, 32><<<blocks, block, 0, stream>>>(a, k, per, turns);
-  else if (groups == 1) kv_append_kernel<F32, FORM, false, 32><<<blocks, block, 0, stream>>>(a, k, per, turns);
-  else kv_append_kernel<F32, FORM, false, 16><<<blocks, block, 0, stream>>>(a, k, per, turns);
+  if (xf) kv_append_kernel<F32, FORM, true, 32><<<blocks, block, 0, stream>>>(a, k, per, more, turns);
+  else if (groups == 1) kv_append_kernel<F32, FORM, false, 32><<<blocks, block, 0, stream>>>(a, k, per, more, turns);
+  else kv_append_kernel<F32, FORM, false, 16><<<blocks, block, 0, stream>>>(a, k, per, more, turns);
 }
 
 cudaError_t launch_kv_append(const KvAppend& a, const KvCache& k, cudaStream_t stream) {
