@@ -346,7 +346,10 @@ int sparse_mqa_attend(const hca_bf16* q, const hca_bf16* kv, long long kv_seq_st
  *                low nibble), scales [n/32] bytes X + 127, rope [rope_dims] bf16
  *                (the first n channels as mxfp4_quantize writes them; n a
  *                positive multiple of 32).  A row is 366 bytes at c = 512 with
- *                64 rotary channels.
+ *                64 rotary channels.  A scale byte is at most 254.
+ * FP8 keeps a NaN, and an infinity makes its group's 64 channels NaN.  FP4 has
+ * no code for either: a NaN is taken for the largest magnitude of its group, and
+ * an infinity's group reads back as infinities and zeros.
  * ld_codes is in bf16 elements (BF16) or bytes, ld_scales in f32 (FP8) or bytes
  * (FP4), ld_rope in bf16 elements.  Rows of codes and of rope start on 16-byte
  * boundaries.  c is a multiple of 8, at most 512; rope_dims a multiple of 8,
@@ -394,7 +397,7 @@ typedef struct {
  *   rope_dims channels turn by their position with base rope_base.  With either,
  *   the stored form is that of the value rounded to bf16, i.e. the cache holds
  *   what rms_norm_rope followed by kv_fp8_quantize or mxfp4_quantize gives;
- *   with neither, that of x.  x does not overlap the cache; two requests of one
+ *   with neither, that of x.  n_rows <= 2^30.  x does not overlap the cache; two requests of one
  *   call do not name the same row (a block shared by their tables is appended to
  *   by one of them at most).
  *
@@ -402,7 +405,7 @@ typedef struct {
  *   out[b*seq_stride_out + j*ld_out ..] for b < B <= n_req, j < n_out is request
  *   b's entry idx[b][j] (idx [B][n_out] int32), or first[b] + j, or j with both
  *   NULL.  A negative entry, a negative first[b] and an entry without a row give
- *   zeros.
+ *   zeros.  B*n_out <= 2^31 - 256; the rows of out do not overlap.
  *
  * sparse_mqa_attend_fp4 -- sparse_mqa_attend over the entries of a FP4 cache, for
  *   decode and for several queries a request (a chunk of a prompt, speculative
@@ -418,7 +421,9 @@ typedef struct {
  *   sparse_mqa_attend.  cfg gives c (= cache->c), n_heads (1 to 128), n_win,
  *   scale, and with rotate_out rope_dims and rope_base; its other fields are not
  *   read.  c is a multiple of 32; scales are 16-byte aligned and ld_scales a
- *   multiple of 16; n_idx <= 4096.  The entries are widened on chip (exactly) and
+ *   multiple of 16; n_idx <= 4096, Tq and n_win <= 2^20, N <= 2^30, and the cache
+ *   has fewer than 2^31 rows.  out overlaps no input.  A row that is not finite
+ *   reaches the queries that see it and no other.  The entries are widened on chip (exactly) and
  *   multiplied in bf16; logits, softmax and sums are f32, and the probabilities
  *   enter the second product rounded to bf16, as the sum they are divided by.
  *   ws: sparse_mqa_attend_fp4_workspace(cfg, Tq, N, n_idx) bytes (n_idx = 0
@@ -527,7 +532,8 @@ typedef struct {
    * their own arrangement), or NULL: the layer's entries are read from them (csa_kv /
    * hca_kv, csa_kv8 / hca_kv8 are not given) as in sparse_mqa_attend_fp4, whether the
    * indexer's keys are flat, paged (block_table) or MXFP4.  With hca_block_cand the
-   * newest HCA entry is appended as entry hca_N-1. */
+   * newest HCA entry is appended as entry hca_N-1.  The caches have room for csa_N /
+   * hca_N entries of B requests; with csa_norm / hca_norm their rope_dims is cfg's. */
   const hca_kv_cache* csa_kv4;
   const hca_kv_cache* hca_kv4;
 } hca_decode_args;

@@ -749,7 +749,7 @@ static KvCache kv_cache_of(const hca_kv_cache* d) {
   return k;
 }
 
-constexpr int kMaxFp4Queries = 1 << 20;
+constexpr int kMaxFp4Queries = 1 << 20, kMaxFp4Entries = 1 << 30;
 // The layer fields that the attention over FP4 entries reads.
 static int check_fp4_cfg(const hca_layer_cfg* cfg, const char* who) {
   CHECK(cfg != nullptr, HCA_ERR_INVALID_ARG, "%s: cfg null", who);
@@ -757,6 +757,8 @@ static int check_fp4_cfg(const hca_layer_cfg* cfg, const char* who) {
   CHECK(cfg->scale > 0.f, HCA_ERR_INVALID_ARG, "%s: cfg scale must be positive", who);
   CHECK(cfg->c % 32 == 0 && cfg->c <= 512 && cfg->n_heads <= 128, HCA_ERR_UNSUPPORTED,
         "%s: cfg c=%d n_heads=%d (c a multiple of 32, at most 512; at most 128 heads)", who, cfg->c, cfg->n_heads);
+  CHECK(cfg->n_win <= kMaxFp4Queries, HCA_ERR_UNSUPPORTED, "%s: cfg n_win=%d (at most %d)", who, cfg->n_win,
+        kMaxFp4Queries);
   return HCA_OK;
 }
 
@@ -785,6 +787,22 @@ static int check_kv4(const hca_layer_cfg* cfg, const hca_kv_cache* k, int n_req,
   CHECK(aligned16(k->scales) && k->ld_scales % 16 == 0, HCA_ERR_INVALID_ARG,
         "%s: cache scales not 16-byte aligned, or ld_scales %lld not a multiple of 16", who, k->ld_scales);
   CHECK(n_req <= k->n_req, HCA_ERR_INVALID_ARG, "%s: cache of %d requests for %d", who, k->n_req, n_req);
+  return HCA_OK;
+}
+
+// One that a layer of the decode call reads: N entries a request, and a window block of n_win rows beside them.
+static int check_decode_kv4(const hca_layer_cfg* cfg, const hca_kv_cache* k, int B, int N, long long win_stride,
+                            bool norm, const char* who) {
+  const int s = check_kv4(cfg, k, B, who);
+  if (s != HCA_OK) return s;
+  const long long room = k->block_table ? (k->bt_stride > (1 << 30) ? 1ll << 30 : k->bt_stride) * k->rows_per_block
+                                        : k->seq_rows;
+  CHECK(N <= kMaxFp4Entries && N <= room, HCA_ERR_INVALID_ARG, "%s: %d entries in a cache with room for %lld", who, N,
+        room);
+  CHECK(win_stride >= (long long)cfg->n_win * cfg->c || B <= 1, HCA_ERR_INVALID_ARG, "%s: window stride %lld", who,
+        win_stride);
+  CHECK(!norm || k->rope_dims == cfg->rope_dims, HCA_ERR_INVALID_ARG, "%s: cache rope_dims=%d, cfg rope_dims=%d", who,
+        k->rope_dims, cfg->rope_dims);
   return HCA_OK;
 }
 
@@ -1024,15 +1042,15 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
     CHECK(!a->block_table, HCA_ERR_UNSUPPORTED, "hybrid_attn_decode: FP8 caches are not paged");
   if (a->csa_q && a->csa_kv4) {
     CHECK(!a->csa_kv8, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: both csa_kv8 and csa_kv4 given");
-    if ((s = check_kv4(cfg, a->csa_kv4, a->B, "hybrid_attn_decode: csa_kv4")) != HCA_OK) return s;
-    CHECK(a->csa_win_stride >= (long long)cfg->n_win * cfg->c || a->B <= 1, HCA_ERR_INVALID_ARG,
-          "hybrid_attn_decode: csa_win_stride %lld", a->csa_win_stride);
+    if ((s = check_decode_kv4(cfg, a->csa_kv4, a->B, a->csa_N, a->csa_win_stride, a->csa_norm != nullptr,
+                              "hybrid_attn_decode: csa_kv4")) != HCA_OK)
+      return s;
   }
   if (a->hca_q && a->hca_kv4) {
     CHECK(!a->hca_kv8, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: both hca_kv8 and hca_kv4 given");
-    if ((s = check_kv4(cfg, a->hca_kv4, a->B, "hybrid_attn_decode: hca_kv4")) != HCA_OK) return s;
-    CHECK(a->hca_win_stride >= (long long)cfg->n_win * cfg->c || a->B <= 1, HCA_ERR_INVALID_ARG,
-          "hybrid_attn_decode: hca_win_stride %lld", a->hca_win_stride);
+    if ((s = check_decode_kv4(cfg, a->hca_kv4, a->B, a->hca_N, a->hca_win_stride, a->hca_norm != nullptr,
+                              "hybrid_attn_decode: hca_kv4")) != HCA_OK)
+      return s;
   }
   if (a->csa_q && a->csa_kv8 && (s = check_kv8(cfg, a->csa_kv8, "hybrid_attn_decode: csa_kv8")) != HCA_OK) return s;
   if (a->hca_q && a->hca_kv8 && (s = check_kv8(cfg, a->hca_kv8, "hybrid_attn_decode: hca_kv8")) != HCA_OK) return s;
@@ -1055,17 +1073,15 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
       CHECK(a->csa_k_stride % 8 == 0, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: csa_k_stride");
     }
     CHECK_PTR(a->csa_topk_idx, "hybrid_attn_decode: csa_topk_idx");
-    s = check_mqa(cfg, a->csa_q, a->csa_kv, a->csa_kv_stride, a->csa_kv8 || a->csa_kv4 ? 0 : a->csa_N, a->csa_topk_idx, cfg->topk,
-                  cfg->m,
-                  a->csa_win, a->csa_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->csa_out, "hybrid_attn_decode: csa");
+    s = check_mqa(cfg, a->csa_q, a->csa_kv, a->csa_kv_stride, a->csa_kv8 || a->csa_kv4 ? 0 : a->csa_N,
+                  a->csa_topk_idx, cfg->topk, cfg->m, a->csa_win, a->csa_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->csa_out, "hybrid_attn_decode: csa");
     if (s != HCA_OK) return s;
     if (a->csa_norm) CHECK_PTR(a->csa_norm, "hybrid_attn_decode: csa_norm");
   }
   if (a->hca_q) {
     CHECK(a->hca_N > 0, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: hca_N=%d", a->hca_N);
-    s = check_mqa(cfg, a->hca_q, a->hca_kv, a->hca_kv_stride, a->hca_kv8 || a->hca_kv4 ? 0 : a->hca_N, nullptr, 0, cfg->m_hca,
-                  a->hca_win,
-                  a->hca_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->hca_out, "hybrid_attn_decode: hca");
+    s = check_mqa(cfg, a->hca_q, a->hca_kv, a->hca_kv_stride, a->hca_kv8 || a->hca_kv4 ? 0 : a->hca_N, nullptr, 0,
+                  cfg->m_hca, a->hca_win, a->hca_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->hca_out, "hybrid_attn_decode: hca");
     if (s != HCA_OK) return s;
     if (a->hca_norm) CHECK_PTR(a->hca_norm, "hybrid_attn_decode: hca_norm");
     if (a->hca_block_cand) {
@@ -1606,8 +1622,8 @@ static size_t fp4_ws(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
 }
 
 size_t sparse_mqa_attend_fp4_workspace(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
-  if (check_fp4_cfg(cfg, "sparse_mqa_attend_fp4") != HCA_OK || Tq < 0 || Tq > kMaxFp4Queries || N < 0 || n_idx < 0 ||
-      n_idx > 4096)
+  if (check_fp4_cfg(cfg, "sparse_mqa_attend_fp4") != HCA_OK || Tq < 0 || Tq > kMaxFp4Queries || N < 0 ||
+      N > kMaxFp4Entries || n_idx < 0 || n_idx > 4096)
     return (size_t)-1;
   return fp4_ws(cfg, Tq, N, n_idx);
 }
@@ -1622,8 +1638,8 @@ int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, c
   int s = check_fp4_cfg(cfg, who);
   if (s != HCA_OK) return s;
   if ((s = check_kv4(cfg, cache, 0, who)) != HCA_OK) return s;
-  CHECK(Tq >= 0 && Tq <= kMaxFp4Queries && N >= 0 && rate >= 1, HCA_ERR_INVALID_ARG, "%s: Tq=%d (at most %d) N=%d rate=%d",
-        who, Tq, kMaxFp4Queries, N, rate);
+  CHECK(Tq >= 0 && Tq <= kMaxFp4Queries && N >= 0 && N <= kMaxFp4Entries && rate >= 1, HCA_ERR_INVALID_ARG,
+        "%s: Tq=%d (at most %d) N=%d (at most %d) rate=%d", who, Tq, kMaxFp4Queries, N, kMaxFp4Entries, rate);
   CHECK(idx ? (n_idx > 0 && n_idx <= 4096) : n_idx == 0, HCA_ERR_INVALID_ARG, "%s: n_idx=%d", who, n_idx);
   CHECK(q_req || Tq <= cache->n_req, HCA_ERR_INVALID_ARG, "%s: %d queries for %d requests without q_req", who, Tq,
         cache->n_req);

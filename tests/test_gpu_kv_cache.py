@@ -286,3 +286,35 @@ def test_debug_check_reports_rows_without_a_place(monkeypatch):
     hca.kv_cache_append(x, k.handle, torch.tensor([7, 8], dtype=torch.int32, device="cuda"))
     assert hca.lib.hca_check_device() == -5 and "no place" in hca.last_error()
     assert hca.lib.hca_check_device() == 0
+
+
+def test_values_that_are_not_finite():
+    """bf16 and FP8 keep a NaN; an infinity stays in bf16 and makes its group of 64 channels NaN in FP8; other groups and
+    rows are untouched.  FP4 gives finite values of the group's largest magnitude there."""
+    import long_context_attention_compress_b200 as hca
+    for form in ("bf16", "fp8", "fp4"):
+        g = torch.Generator().manual_seed(5)
+        x = torch.randn(6, 512, generator=g)
+        good = x.clone()
+        x[0, 5], x[1, 70], x[2, 511], x[3, 500] = float("nan"), float("inf"), float("nan"), float("-inf")
+        out = []
+        for rows in (x, good):
+            k = Cache(form, 512, 64, 1, 6)
+            hca.kv_cache_append(rows.cuda(), k.handle, torch.zeros(1, dtype=torch.int32).cuda(),
+                                row_start=torch.tensor([0, 6], dtype=torch.int32).cuda())
+            out.append(hca.kv_cache_gather(k.handle, 1, 6)[0].float().cpu())
+        y, z = out
+        same = torch.ones(6, 512, dtype=torch.bool)
+        n = {"bf16": 1, "fp8": 64, "fp4": 32}[form]
+        same[0, 5 // n * n:5 // n * n + n] = False
+        same[1, 70 // n * n:70 // n * n + n] = False
+        same[2, 511] = same[3, 500] = False
+        assert torch.equal(y[same], z[same])
+        assert torch.isnan(y[2, 511]) and y[3, 500] == float("-inf")  # rotary channels are bf16
+        if form == "bf16":
+            assert torch.isnan(y[0, 5]) and y[1, 70] == float("inf")
+        elif form == "fp8":
+            assert torch.isnan(y[0, 5]) and torch.isnan(y[1, 64:128]).all()
+            assert torch.isfinite(y[0, 6:]).all()
+        else:
+            assert torch.isfinite(y[0, :448]).all() and torch.isfinite(y[1, :64]).all()

@@ -340,3 +340,43 @@ def test_index_check(monkeypatch):
     got = s.call(pos, idx=np.concatenate([idx, ok[:, 32:]], 1))
     assert hca.lib.hca_check_device() == -5 and "block-table" in hca.last_error()
     s.check(got, pos, idx=idx)
+
+
+def test_pool_longer_than_32_bits_of_bytes():
+    """Entries at the far end of a pool of 20 M rows (4.5 GB of codes): appended there, attended from there."""
+    import long_context_attention_compress_b200 as hca
+    n_blocks, rpb, N, H = 625_000, 32, 300, 16
+    t = {"codes": torch.empty((n_blocks, rpb, 224), dtype=torch.uint8, device="cuda"),
+         "scales": torch.empty((n_blocks, rpb, 16), dtype=torch.uint8, device="cuda"),
+         "rope": torch.empty((n_blocks, rpb, 64), dtype=torch.bfloat16, device="cuda")}
+    per = -(-N // rpb)
+    table = torch.arange(n_blocks - 2 * per, n_blocks, dtype=torch.int32, device="cuda").reshape(2, per)
+    k = hca.KvCache("fp4", 512, 64, **t, block_table=table)
+    g = torch.Generator().manual_seed(3)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    hca.kv_cache_append(torch.randn(2 * N, 512, generator=g).cuda(), k, i32([0, 0]), row_start=i32([0, N, 2 * N]))
+    back = to64(hca.kv_cache_gather(k, 2, N))
+    assert all(np.abs(back[b]).max() > 1 for b in range(2))
+    q = torch.randn(2, H, 512, generator=g).bfloat16()
+    cfg = make(512, H)
+    got = to64(hca.sparse_mqa_attend_fp4(q.cuda(), k, N, i32([1199, 800]), cfg, rate=4))
+    for b, n in enumerate((300, 200)):
+        check_query(got[b], to64(q[b]), back[b, :n], cfg.scale, what=f"query {b}")
+
+
+def test_two_streams_at_once():
+    """Calls that run side by side on two streams, each with its workspace, give what they give alone."""
+    a, b = Setup(N=900, B=4, rpb=32, seed=1), Setup(N=700, H=16, B=2, nq=8, seed=2)
+    calls = [lambda: a.call([3599, 3000, 64, 2000]),
+             lambda: b.call([1500 + i % 8 for i in range(16)], q_req=[i // 8 for i in range(16)])]
+    alone = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for f, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(f())
+        torch.cuda.synchronize()
+        for x, y in zip(alone, got):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))

@@ -129,6 +129,9 @@ def test_attend_refusals(lib):
     assert call(d=desc(lib, 0)) == -2 and call(d=desc(lib, 1)) == -2 and call(d=desc(lib, ring=1)) == -2
     assert call(d=desc(lib, scales=FAKE + 8)) == -1 and call(d=desc(lib, ld_scales=14)) == -1
     assert call(Tq=-1) == -1 and call(N=-1) == -1 and call(rate=0) == -1
+    assert call(N=(1 << 30) + 1) == -1 and call(Tq=(1 << 20) + 1, req=FAKE) == -1
+    assert call(cfg=cfg(n_win=(1 << 20) + 1), W=(1 << 20) + 1, ws_=((1 << 20) + 1) * 512) == -2
+    assert lib.sparse_mqa_attend_fp4_workspace(cfg(), 4, (1 << 30) + 1, 0) == lib.SIZE_MAX
     assert call(idx=FAKE) == -1 and call(k=5) == -1 and call(idx=FAKE, k=4097) == -1
     assert call(Tq=5) == -1 and "q_req" in lib.last_error()
     assert call(W=127) == -1 and call(ws_=128 * 512 + 4) == -1 and call(ws_=128 * 512 - 8) == -1
@@ -138,6 +141,47 @@ def test_attend_refusals(lib):
     assert call(pos=None) == -1 and call(pos=FAKE + 2) == -1 and call(req=FAKE + 1) == -1 and call(sink=FAKE + 2) == -1
     assert call(idx=FAKE + 2, k=4) == -1
     assert call(ws=None) == -1 and call(ws=FAKE + 128) == -1
+
+
+def test_layer_decode_refusals(lib):
+    """csa_kv4 / hca_kv4 of hybrid_attn_decode: each bad cache is refused by the call, and those that change the plan by
+    the workspace query too."""
+    from types import SimpleNamespace
+    cfg = lib.make_cfg(SimpleNamespace(c=512, m=4, m_hca=128, topk=64, n_idx_heads=64, d_idx=128, n_heads=64, n_win=128,
+                                       scale=512 ** -0.5, rope_dims=64, rope_base=1e4, norm_eps=1e-6))
+    kv8 = lib.KvFp8()
+
+    def call(layer, d, B=2, query=False, **kw):
+        a = lib.DecodeArgs()
+        a.B, a.q_pos = B, FAKE
+        names = dict(q=FAKE, out=FAKE, N=8192, win=FAKE, win_stride=128 * 512)
+        if layer == "csa":
+            names.update(q_idx=FAKE, w_idx=FAKE, k_idx=FAKE, k_stride=128 * 128, topk_idx=FAKE)
+        names.update(kw)
+        for k, v in names.items():
+            setattr(a, f"{layer}_{k}", v)
+        setattr(a, f"{layer}_kv4", ctypes.addressof(d))
+        if query:
+            return lib.hybrid_attn_decode_workspace(cfg, a)
+        return lib._decode(ctypes.byref(cfg), ctypes.byref(a), None, 0, None)
+
+    for layer in ("csa", "hca"):
+        cache = lambda **kw: desc(lib, **dict(dict(n_rows=4 * 8192, seq_rows=8192), **kw))  # noqa: E731
+        assert 0 < call(layer, cache(), query=True) < lib.SIZE_MAX
+        assert call(layer, cache()) == -3 and "workspace" in lib.last_error()    # everything else is in order
+        assert call(layer, cache(block_table=FAKE, bt_stride=1024, rows_per_block=8)) == -3
+        for st, kw in [(-2, dict(form=0)), (-2, dict(form=1)), (-2, dict(ring=1)), (-1, dict(c=256, rope_dims=64, ld_codes=96)),
+                       (-1, dict(n_req=1, n_rows=8192)), (-1, dict(scales=FAKE + 8)), (-1, dict(ld_scales=24)),
+                       (-2, dict(n_rows=1 << 31)), (-1, dict(codes=None))]:
+            d = cache(**kw)
+            assert call(layer, d) == st, (layer, kw, lib.last_error())
+            assert call(layer, d, query=True) == lib.SIZE_MAX, (layer, kw)
+        assert call(layer, cache(), N=8193) == -1 and "room" in lib.last_error()
+        assert call(layer, cache(block_table=FAKE, bt_stride=1023, rows_per_block=8)) == -1
+        assert call(layer, cache(), win_stride=127 * 512) == -1
+        assert call(layer, cache(), kv8=ctypes.addressof(kv8)) == -1 and "both" in lib.last_error()
+        assert call(layer, cache(rope_dims=0, ld_codes=256), norm=FAKE) == -1 and "rope_dims" in lib.last_error()
+        assert call(layer, cache(rope_dims=0, ld_codes=256)) == -3
 
 
 def test_fault_injection(lib, monkeypatch):
