@@ -169,10 +169,15 @@ def _ptr(t, dtype=None, name="tensor"):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _current_device():
+    # (torch.cuda.current_device() costs three times as much; CUDA is up where a tensor lives on it)
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _stream(stream=None, device=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -357,11 +362,26 @@ _FORMS = {"bf16": HCA_KV_BF16, "fp8": HCA_KV_FP8, "fp4": HCA_KV_FP4}
 
 
 def _same_device(*tensors):
-    """The kernels run on the current device's stream: every tensor has to live on that device."""
-    cur = torch.cuda.current_device()
+    """The kernels run on the current device's stream: every tensor has to live on that device, whose number it returns."""
+    cur = _current_device()
     for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, but the current device is cuda:{cur}")
+        if t is not None:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
+            if t.get_device() != cur:
+                raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, but the current device is cuda:{cur}")
+    return cur
+
+
+def _arg(t, dtype, name):
+    """_ptr of a tensor that _same_device has seen."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
 
 
 def _scratch(need: int, device, stream):
@@ -438,26 +458,27 @@ def kv_cache_append(x, cache: KvCache, first, row_start=None, rate=1, gamma=None
     """Append rows x [n, c] (bf16 or float32) to a cache: request b's rows x[row_start[b]:row_start[b+1]] (one row a
     request without row_start) become its entries first[b], first[b] + 1, ...; entry e is normalised with gamma [c]
     float32 if given and, with rotate, turned by position (e+1)*rate - 1 on the way.  first, row_start: int32."""
-    if x.dtype not in (BF16, F32):
-        raise TypeError(f"x: dtype {x.dtype}")
-    if x.dim() != 2 or x.shape[1] != cache.c or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"x: shape {tuple(x.shape)}, strides {x.stride()}; expected rows of {cache.c} channels")
-    _same_device(cache.codes, x, first, row_start, gamma)
+    dev = _same_device(cache.codes, x, first, row_start, gamma)
+    dtype, shape, strides = x.dtype, x.shape, x.stride()
+    if dtype is not BF16 and dtype is not F32:
+        raise TypeError(f"x: dtype {dtype}")
+    if len(shape) != 2 or shape[1] != cache.c or (shape[1] > 1 and strides[1] != 1):
+        raise ValueError(f"x: shape {tuple(shape)}, strides {strides}; expected rows of {cache.c} channels")
     B = first.numel()
     if row_start is not None and row_start.numel() != B + 1:
         raise ValueError(f"row_start: {row_start.numel()} values for {B} requests")
     if gamma is not None and gamma.numel() != cache.c:
         raise ValueError(f"gamma: {gamma.numel()} weights for {cache.c} channels")
-    _check(_kv_append(x.data_ptr(), 1 if x.dtype == F32 else 0, x.stride(0) if x.shape[0] > 1 else cache.c, x.shape[0],
-                      _ptr(row_start, I32, "row_start"), _ptr(first, I32, "first"), B, int(rate),
-                      _ptr(gamma, F32, "gamma"), float(norm_eps), 1 if rotate else 0, float(rope_base),
-                      cache.ref, _stream(stream)))
+    _check(_kv_append(x.data_ptr(), 1 if dtype is F32 else 0, strides[0] if shape[0] > 1 else cache.c, shape[0],
+                      _arg(row_start, I32, "row_start"), _arg(first, I32, "first"), B, int(rate),
+                      _arg(gamma, F32, "gamma"), float(norm_eps), 1 if rotate else 0, float(rope_base),
+                      cache.ref, _stream(stream, dev)))
 
 
 def kv_cache_gather(cache: KvCache, B, n_out, idx=None, first=None, out=None, stream=None):
     """Rows of a cache as bf16 [B, n_out, c]: request b's entries idx[b] ([B, n_out] int32; negative: a zero row), or
     first[b] + j ([B] int32), or j."""
-    _same_device(cache.codes, idx, first, out)
+    dev = _same_device(cache.codes, idx, first, out)
     if idx is not None and tuple(idx.shape) != (B, n_out):
         raise ValueError(f"idx: shape {tuple(idx.shape)}, expected {(B, n_out)}")
     if first is not None and first.numel() != B:
@@ -466,8 +487,8 @@ def kv_cache_gather(cache: KvCache, B, n_out, idx=None, first=None, out=None, st
         out = torch.empty((B, n_out, cache.c), dtype=BF16, device=cache.codes.device)
     elif tuple(out.shape) != (B, n_out, cache.c):
         raise ValueError(f"out: shape {tuple(out.shape)}, expected {(B, n_out, cache.c)}")
-    _check(_kv_gather(cache.ref, int(B), int(n_out), _ptr(idx, I32, "idx"), _ptr(first, I32, "first"),
-                      _ptr(out, BF16, "out"), cache.c, n_out * cache.c, _stream(stream)))
+    _check(_kv_gather(cache.ref, int(B), int(n_out), _arg(idx, I32, "idx"), _arg(first, I32, "first"),
+                      _arg(out, BF16, "out"), cache.c, n_out * cache.c, _stream(stream, dev)))
     return out
 
 
@@ -482,7 +503,7 @@ def sparse_mqa_attend_fp4(q, cache: KvCache, N, q_pos, cfg: LayerCfg, idx=None, 
     the request of each query (None: query i belongs to request i).  Other arguments as in sparse_mqa_attend."""
     if q.dim() != 3 or tuple(q.shape[1:]) != (cfg.n_heads, cfg.c):
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [Tq, {cfg.n_heads}, {cfg.c}]")
-    _same_device(cache.codes, q, q_pos, idx, win, q_req, sink, out, ws)
+    dev = _same_device(cache.codes, q, q_pos, idx, win, q_req, sink, out, ws)
     Tq = q.shape[0]
     for name, t in (("q_pos", q_pos), ("q_req", q_req)):
         if t is not None and t.numel() != Tq:
@@ -504,11 +525,11 @@ def sparse_mqa_attend_fp4(q, cache: KvCache, N, q_pos, cfg: LayerCfg, idx=None, 
         ws, nb = _scratch(sparse_mqa_attend_fp4_workspace(cfg, Tq, N, n_idx), q.device, stream)
     else:
         nb = ws.numel() * ws.element_size()
-    _check(_mqa_fp4(_ptr(q, BF16, "q"), cache.ref, int(N), _ptr(idx, I32, "idx"), n_idx, int(rate),
-                    _ptr(win, BF16, "win"), 0 if win is None else win.shape[1] * win.shape[2],
-                    0 if win is None else win.shape[1], _ptr(q_pos, I32, "q_pos"), _ptr(q_req, I32, "q_req"), Tq,
-                    ctypes.byref(cfg), _ptr(sink, F32, "sink"), 1 if rotate_out else 0, _ptr(out, BF16, "out"),
-                    None if ws is None else ws.data_ptr(), nb, _stream(stream)))
+    _check(_mqa_fp4(_arg(q, BF16, "q"), cache.ref, int(N), _arg(idx, I32, "idx"), n_idx, int(rate),
+                    _arg(win, BF16, "win"), 0 if win is None else win.shape[1] * win.shape[2],
+                    0 if win is None else win.shape[1], _arg(q_pos, I32, "q_pos"), _arg(q_req, I32, "q_req"), Tq,
+                    ctypes.byref(cfg), _arg(sink, F32, "sink"), 1 if rotate_out else 0, _arg(out, BF16, "out"),
+                    None if ws is None else ws.data_ptr(), nb, _stream(stream, dev)))
     return out
 
 

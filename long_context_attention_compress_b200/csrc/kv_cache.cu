@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "formats.cuh"
@@ -113,6 +114,9 @@ __device__ __forceinline__ uint2 e4m3x8_encode(const float* y, float sc) {
 struct Turns {
   double hi[kKvMaxPairs], lo[kKvMaxPairs];
 };
+struct NoTurns {};  // (a launch that only converts does not carry the table)
+template <bool XF>
+using TurnsOf = std::conditional_t<XF, Turns, NoTurns>;
 
 // Resident blocks per SM that the registers are held to.
 constexpr int append_blocks(int form, bool xf) { return xf ? 6 : form == HCA_KV_FP8 ? 8 : 10; }
@@ -121,7 +125,7 @@ constexpr int append_blocks(int form, bool xf) { return xf ? 6 : form == HCA_KV_
 // channels that are only converted (the indexer's keys), else 32.
 template <bool F32, int FORM, bool XF, int LANES>
 __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
-    kv_append_kernel(KvAppend a, KvCache k, int base_rows, int one_more, const __grid_constant__ Turns turns) {
+    kv_append_kernel(KvAppend a, KvCache k, int base_rows, int one_more, const __grid_constant__ TurnsOf<XF> turns) {
   constexpr int kU = LANES == 32 ? kKvChunks : 1;  // chunks per lane
   __shared__ double2 s_cs[XF ? kKvWarps : 1][kKvMaxPairs];  // cosine and sine of each pair at the warp's position
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, sub = lane & (LANES - 1);
@@ -481,16 +485,17 @@ const Turns& turns_of(int rope_dims, float base) {
 template <bool F32, int FORM>
 static void append_rows(const KvAppend& a, const KvCache& k, cudaStream_t stream) {
   const bool xf = a.gamma || (a.rotate && k.rope_dims > 0);
-  const Turns& turns = turns_of(a.rotate ? k.rope_dims : 0, a.rope_base);
   // one row a group of lanes until the machine is full (the resident warps of the launch bounds), then contiguous runs
   const int groups = !xf && k.c <= 128 ? 2 : 1;  // per warp
   const int max_groups = device_sm_count() * kKvWarps * append_blocks(FORM, xf) * groups;
   const int used = std::min(a.n_rows, max_groups), per = a.n_rows / used, more = a.n_rows - per * used;
   const int blocks = (used + kKvWarps * groups - 1) / (kKvWarps * groups);
   const dim3 block(32 * kKvWarps);
-  if (xf) kv_append_kernel<F32, FORM, true, 32><<<blocks, block, 0, stream>>>(a, k, per, more, turns);
-  else if (groups == 1) kv_append_kernel<F32, FORM, false, 32><<<blocks, block, 0, stream>>>(a, k, per, more, turns);
-  else kv_append_kernel<F32, FORM, false, 16><<<blocks, block, 0, stream>>>(a, k, per, more, turns);
+  if (xf)
+    kv_append_kernel<F32, FORM, true, 32><<<blocks, block, 0, stream>>>(
+        a, k, per, more, turns_of(a.rotate ? k.rope_dims : 0, a.rope_base));
+  else if (groups == 1) kv_append_kernel<F32, FORM, false, 32><<<blocks, block, 0, stream>>>(a, k, per, more, NoTurns{});
+  else kv_append_kernel<F32, FORM, false, 16><<<blocks, block, 0, stream>>>(a, k, per, more, NoTurns{});
 }
 
 cudaError_t launch_kv_append(const KvAppend& a, const KvCache& k, cudaStream_t stream) {
