@@ -744,7 +744,7 @@ static KvCache kv_cache_of(const hca_kv_cache* d) {
   k.bt_stride = d->bt_stride;
   k.rpb = d->block_table ? d->rows_per_block : 1;
   // (a ring of 2^31 rows or more never wraps: entries are 32-bit)
-  k.div = fast_div(d->block_table ? (uint32_t)d->rows_per_block : (uint32_t)std::min(std::max(d->seq_rows, 1ll), 1ll << 31));
+  k.div = fast_div((uint32_t)(d->block_table ? d->rows_per_block : std::min(std::max(d->seq_rows, 1ll), 1ll << 31)));
   k.n_req = d->n_req;
   return k;
 }
@@ -1074,14 +1074,16 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
     }
     CHECK_PTR(a->csa_topk_idx, "hybrid_attn_decode: csa_topk_idx");
     s = check_mqa(cfg, a->csa_q, a->csa_kv, a->csa_kv_stride, a->csa_kv8 || a->csa_kv4 ? 0 : a->csa_N,
-                  a->csa_topk_idx, cfg->topk, cfg->m, a->csa_win, a->csa_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->csa_out, "hybrid_attn_decode: csa");
+                  a->csa_topk_idx, cfg->topk, cfg->m, a->csa_win, a->csa_win_stride, a->q_pos, a->B,
+                  HCA_MODE_DECODE, a->csa_out, "hybrid_attn_decode: csa");
     if (s != HCA_OK) return s;
     if (a->csa_norm) CHECK_PTR(a->csa_norm, "hybrid_attn_decode: csa_norm");
   }
   if (a->hca_q) {
     CHECK(a->hca_N > 0, HCA_ERR_INVALID_ARG, "hybrid_attn_decode: hca_N=%d", a->hca_N);
     s = check_mqa(cfg, a->hca_q, a->hca_kv, a->hca_kv_stride, a->hca_kv8 || a->hca_kv4 ? 0 : a->hca_N, nullptr, 0,
-                  cfg->m_hca, a->hca_win, a->hca_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->hca_out, "hybrid_attn_decode: hca");
+                  cfg->m_hca, a->hca_win, a->hca_win_stride, a->q_pos, a->B, HCA_MODE_DECODE, a->hca_out,
+                  "hybrid_attn_decode: hca");
     if (s != HCA_OK) return s;
     if (a->hca_norm) CHECK_PTR(a->hca_norm, "hybrid_attn_decode: hca_norm");
     if (a->hca_block_cand) {
@@ -1224,7 +1226,8 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
       p.win_seq_stride = (long long)nw * c;
       p.rope_dims = cfg->rope_dims;
     }
-    return cuda_status(launch_mqa_fp4(p, pl, aws, sm), csa ? "decode: csa attention (fp4)" : "decode: hca attention (fp4)");
+    return cuda_status(launch_mqa_fp4(p, pl, aws, sm),
+                       csa ? "decode: csa attention (fp4)" : "decode: hca attention (fp4)");
   };
   auto run_hca_attention = [&]() -> int {
     if (a->hca_kv4) {

@@ -5,20 +5,26 @@
 //   bf16; FP8: scale = f32(amax / 448) per 64 channels, the E4M3 value nearest to y / scale; FP4: 2^X per 32
 //   channels, X = floor(log2 amax) - 2, the E2M1 value nearest to y * 2^-X; the last rope_dims channels bf16.
 // One warp owns a row: lane l holds the 8-channel chunks l and l + 32, so a group's maximum is two (FP4) or three
-// (FP8) shuffles away and nothing passes through memory between the input and the stored row.  Bound by HBM for many
-// rows (c*4 B in, 366 B out for FP4 at c = 512), by latency for few.
+// (FP8) shuffles away and nothing passes through memory between the input and the stored row; rows of at most 128
+// channels that are only converted take half a warp.  The next row's load is always under way.
 // Roundings.  With normalisation or rotation y is rounded to bf16 first (what the bf16 cache holds), as from the
 // float64 value: a quantised code must not depend on which side of a midpoint an f32 normalisation falls.  Sum of
 // squares and rotation are f64; the other channels are formed in f32, 8 ulps too low and too high (f32 is within 4),
-// and redone in f64 only where the two round apart.  The codes are those of the stored-form definitions bit for bit: FP4 scaling is
-// exact and the conversion rounds to nearest even; an f32 quotient (by the reciprocal, within 2 ulps) within 4 of an E4M3 midpoint, or in E4M3's
-// subnormal range, is decided on the f64 quotient.
-//
+// and redone in f64 only where the two round apart.  The codes are those of the stored-form definitions bit for bit:
+// FP4 scaling is exact and the conversion rounds to nearest even; an f32 quotient (by the reciprocal, within 2 ulps)
+// that is within 4 ulps of an E4M3 midpoint, or in E4M3's subnormal range, is decided on the f64 quotient.
 // The angle is formed in turns from theta / 2 pi in two f64 words (a table made on the host) with an error-free product,
 // so that its fraction is good to 2^-52 at any position and the sine and cosine need no long reduction.
+// Bound: by HBM only where rows are converted as they are (c*4 B in, 366 B out for FP4 at c = 512); with normalisation
+// and rotation by issue slots, 780 instructions a row at 0.6 a cycle and scheduler.  Measured, c = 512: 16,384 f32 rows
+// normalised to FP4 25.7 us (8.6 us of HBM time), 3,001 to FP8 in 13 ragged requests 7.3 us, 256 bf16 rows into rings
+// 2.0 us, 8 rows 4.5 us: a row's chain of loads, f64 sum, inverse root and sine.  An f32 normalisation with error
+// bounds and f64 behind it for every fifth row had as many instructions and took 28 us for the 16,384.
 //
 // kv_gather_kernel.  The bf16 values of rows.  Each row is a chain of dependent loads (index, block table, row): a block
-// resolves 32 rows at a time, one a thread, while its warps move the 32 before, four rows in flight per warp.
+// resolves 32 rows at a time, one a thread, while its warps move the 32 before, four rows in flight per warp (their
+// loads predicated, not branched around, so that they issue together).  Bound by memory: 8 x 8,191 FP4 rows 19.3 us
+// (4.7 TB/s read and written; 13.9 us at the copy rate), 32 x 1,024 selected FP8 rows 11.1 us (4.8 TB/s).
 
 #include <cuda_fp16.h>
 
@@ -118,8 +124,11 @@ struct NoTurns {};  // (a launch that only converts does not carry the table)
 template <bool XF>
 using TurnsOf = std::conditional_t<XF, Turns, NoTurns>;
 
-// Resident blocks per SM that the registers are held to.
-constexpr int append_blocks(int form, bool xf) { return xf ? 6 : form == HCA_KV_FP8 ? 8 : 10; }
+// Resident blocks per SM that the registers are held to.  Normalised, bf16 form: 7 against 6 took 6.3 against 6.9 us for
+// 4,100 rows; FP8 and FP4, which need a few registers more: 6 against 7 took 25.7 against 26.1 us for 16,384 FP4 rows.
+constexpr int append_blocks(int form, bool xf) {
+  return xf ? (form == HCA_KV_BF16 ? 7 : 6) : form == HCA_KV_FP8 ? 8 : 10;
+}
 
 // XF: with normalisation or rotation; without, a row is only converted.  LANES lanes a row: 16 for rows of at most 128
 // channels that are only converted (the indexer's keys), else 32.
@@ -127,6 +136,7 @@ template <bool F32, int FORM, bool XF, int LANES>
 __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
     kv_append_kernel(KvAppend a, KvCache k, int base_rows, int one_more, const __grid_constant__ TurnsOf<XF> turns) {
   constexpr int kU = LANES == 32 ? kKvChunks : 1;  // chunks per lane
+  __shared__ double2 s_turn[XF ? kKvMaxPairs : 1];
   __shared__ double2 s_cs[XF ? kKvWarps : 1][kKvMaxPairs];  // cosine and sine of each pair at the warp's position
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5, sub = lane & (LANES - 1);
   const unsigned int all = LANES == 32 ? 0xffffffffu : 0xffffu << (lane & 16);  // this row's lanes
@@ -134,18 +144,17 @@ __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
   const int grp = (blockIdx.x * kKvWarps + wib) * (32 / LANES) + lane / LANES;
   const int r0 = grp * base_rows + min(grp, one_more);
   const int r1 = min(a.n_rows, r0 + base_rows + (grp < one_more ? 1 : 0));
+  if constexpr (XF) {
+    if (a.rotate) {
+      for (int j = threadIdx.x; j < k.rope_dims >> 1; j += 32 * kKvWarps)
+        s_turn[j] = make_double2(turns.hi[j], turns.lo[j]);
+      __syncthreads();
+    }
+  }
   if (r0 >= r1) return;
   const int nch = k.c >> 3;
   const int rope0 = k.c - k.rope_dims;
   const int n_pairs = XF && a.rotate ? k.rope_dims >> 1 : 0;
-  double turn_hi[kKvMaxPairs / 32], turn_lo[kKvMaxPairs / 32];  // of pairs lane, lane + 32, ...
-  if constexpr (XF) {
-#pragma unroll
-    for (int u = 0; u < kKvMaxPairs / 32; ++u) {
-      turn_hi[u] = lane + 32 * u < n_pairs ? turns.hi[lane + 32 * u] : 0.0;
-      turn_lo[u] = lane + 32 * u < n_pairs ? turns.lo[lane + 32 * u] : 0.0;
-    }
-  }
   const double inv_c = 1.0 / k.c;
   // The next row is always under way: its load depends on nothing else.
   float next[kU][8];
@@ -209,11 +218,12 @@ __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
       if (n_pairs > 0) {
         const double pos = (double)((e + 1) * a.rate - 1);
         __syncwarp();  // the last row's table has been read
-#pragma unroll
-        for (int u = 0; u < kKvMaxPairs / 32; ++u) {
+#pragma unroll 1
+        for (int u = 0; 32 * u < n_pairs; ++u) {
           if (lane + 32 * u < n_pairs) {
-            const double t = pos * turn_hi[u];
-            const double rest = fma(pos, turn_lo[u], fma(pos, turn_hi[u], -t));  // what t lacks
+            const double2 turn = s_turn[lane + 32 * u];
+            const double t = pos * turn.x;
+            const double rest = fma(pos, turn.y, fma(pos, turn.x, -t));  // what t lacks
             double sn, cs;
             sincospi(2.0 * ((t - rint(t)) + rest), &sn, &cs);
             s_cs[wib][lane + 32 * u] = make_double2(cs, sn);
@@ -377,10 +387,9 @@ constexpr int kGatherBlock = 8 * kGatherRows;        // rows a block takes at a 
 constexpr int kGatherResident = 3;                   // blocks per SM
 
 template <int FORM>
-__global__ void __launch_bounds__(256, kGatherResident) kv_gather_kernel(KvCache k, FastDiv n_out, uint32_t total,
-                                                        const int32_t* __restrict__ idx,
-                                                        const int32_t* __restrict__ first, bf16* __restrict__ out,
-                                                        long long ld_out, long long seq_out) {
+__global__ void __launch_bounds__(256, kGatherResident)
+    kv_gather_kernel(KvCache k, FastDiv n_out, uint32_t total, const int32_t* __restrict__ idx,
+                     const int32_t* __restrict__ first, bf16* __restrict__ out, long long ld_out, long long seq_out) {
   __shared__ long long s_row[2][kGatherBlock], s_dst[2][kGatherBlock];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nch = k.c >> 3;
@@ -500,9 +509,12 @@ static void append_rows(const KvAppend& a, const KvCache& k, cudaStream_t stream
 
 cudaError_t launch_kv_append(const KvAppend& a, const KvCache& k, cudaStream_t stream) {
   if (a.n_rows <= 0 || a.B <= 0) return cudaSuccess;
-  if (k.form == HCA_KV_BF16) a.x_f32 ? append_rows<true, HCA_KV_BF16>(a, k, stream) : append_rows<false, HCA_KV_BF16>(a, k, stream);
-  else if (k.form == HCA_KV_FP8) a.x_f32 ? append_rows<true, HCA_KV_FP8>(a, k, stream) : append_rows<false, HCA_KV_FP8>(a, k, stream);
-  else a.x_f32 ? append_rows<true, HCA_KV_FP4>(a, k, stream) : append_rows<false, HCA_KV_FP4>(a, k, stream);
+  if (k.form == HCA_KV_BF16)
+    a.x_f32 ? append_rows<true, HCA_KV_BF16>(a, k, stream) : append_rows<false, HCA_KV_BF16>(a, k, stream);
+  else if (k.form == HCA_KV_FP8)
+    a.x_f32 ? append_rows<true, HCA_KV_FP8>(a, k, stream) : append_rows<false, HCA_KV_FP8>(a, k, stream);
+  else
+    a.x_f32 ? append_rows<true, HCA_KV_FP4>(a, k, stream) : append_rows<false, HCA_KV_FP4>(a, k, stream);
   ++g_launch_counter;
   return cudaGetLastError();
 }
@@ -511,7 +523,8 @@ cudaError_t launch_kv_gather(const KvCache& k, int B, int n_out, const int32_t* 
                              long long ld_out, long long seq_out, cudaStream_t stream) {
   const long long total = (long long)B * n_out;
   if (total <= 0) return cudaSuccess;
-  const unsigned grid = (unsigned)std::min<long long>((total + kGatherBlock - 1) / kGatherBlock, (long long)kGatherResident * device_sm_count());
+  const unsigned grid = (unsigned)std::min<long long>((total + kGatherBlock - 1) / kGatherBlock,
+                                                      (long long)kGatherResident * device_sm_count());
   const FastDiv n = fast_div((uint32_t)n_out);
   const uint32_t rows = (uint32_t)total;
   if (k.form == HCA_KV_BF16)

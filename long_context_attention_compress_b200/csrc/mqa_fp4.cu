@@ -4,6 +4,14 @@
 //   o[t, h, :] = sum_u softmax_u(scale * q[t, h, :] . row_u) row_u
 // An entry's row is code * 2^X per 32 channels on its first c - rope_dims channels and bf16 on the rest; both are
 // exact in bf16.
+//
+// Work: a row is 366 bytes at c = 512 (56 ps of HBM time) and 4*H*c flops a query (78 ps of tensor time at 64 heads),
+// once widened.  Widening is what the two do not show: 14 half-rate byte permutes and 4 multiplies per 8 codes, 1.8 k
+// cycles of an SM's four ALUs per 128 rows, against 0.9 k for the flops at full rate.
+// Roundings: products are exact in f32 and summed in f32 by the tensor cores; logits, softmax, states and sums are f32.
+// P is rounded to bf16 for the second product, and the row sums are those of the rounded P, so a common rounding of
+// all weights cancels; the weights' own roundings (2^-9 on average) come to 2e-3 of the output, where its rounding to
+// bf16 alone is 1.7e-3.
 
 #include <cudaTypedefs.h>
 
@@ -55,7 +63,8 @@ __device__ __forceinline__ const bf16* window_row(const MqaFp4Problem& p, const 
 
 // ---- CUDA cores: c other than 512 ------------------------------------------------------
 // One CTA per (query, group of kSH heads, split): rows are widened into shared memory 16 at a time, an online softmax
-// runs over them, and the state (m, l, o) goes to the combine kernel.
+// runs over them, and the state (m, l, o) goes to the combine kernel.  Bound by f32 FMAs and shared memory: it took
+// 1.2 ms for the 8 x 8,192 entries of c = 512 that take 33.6 us below; the small widths it serves are short.
 constexpr int kSThreads = 256, kSRows = 16, kSH = 4;
 
 __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem p, int splits, int rows_per_split,
@@ -177,6 +186,17 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
 //                 registers while QK^T and the softmax run, so that only stores lie between PV releasing a block
 //                 and the next QK^T over it; rotary channels and window rows are copied with
 //                 16-byte cp.async
+// Where few heads would leave columns empty, they are given to neighbouring queries (see Group below).
+//
+// Measured at 64 heads: 8 requests x 8,192 entries 33.6 us, 32 x 1,024 selected 29.3 us; 16 heads, 2 x 192 queries over
+// 8,192 entries 101 us (284 us with a query a CTA).  Steady state, 6.8 k cycles a tile: softmax 2.3 k (S seen to P
+// signalled, beside the next tile's widening), PV 1.55 k (32 MMAs at 48 cycles: each reads 6 KiB of shared memory), the
+// blocks' refill 2.4 k past PV's end (128 KiB of stores beside the 192 KiB that QK^T reads), QK^T's tail 0.5 k.  Around
+// it 11.5 k cycles before the first P (set-up, the chain q_pos - block table - codes, one tile's widening) and 5 k for
+// 128 KiB of partial states (26 B a cycle and SM, the rate of L2 writes), then the combine.
+// Tried and dropped: QK^T from rows in TMEM with V's stores behind PV (the converters' work comes in series: 45 us);
+// one proxy fence for several blocks, the widening held back until P is signalled, the E2M1 conversion instruction for
+// half of the codes (no gain or slower).
 constexpr int kSoft = 8, kConv = 16;
 constexpr int kThreads = 32 * (4 + kSoft + kConv);   // whole warpgroups, for the register split
 constexpr int kRowsT = 128;                          // rows per tile
@@ -418,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       if (lead) {
         tc::mbar_arrive_expect_tx(&bars->qfull, kQBytes);
         for (int ch = 0; ch < 8; ++ch)
-          tc::tma_load_3d(base + kOffQ + ch * kQChunk, &tm_q, &bars->qfull, ch * 64, PACK ? q0 * p.H : h0, PACK ? 0 : q0);
+          tc::tma_load_3d(base + kOffQ + ch * kQChunk, &tm_q, &bars->qfull, ch * 64, PACK ? q0 * p.H : h0,
+                          PACK ? 0 : q0);
       }
       __syncwarp();
       constexpr uint32_t id_qk = tc::idesc_bf16_f32(kRowsT, kHT, false, false);
@@ -746,7 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
           if (k) atomicOr(&g_mqa_fp4_error, k << 1);
         }
         if (e < 0 || e >= p.N) return -1;
-        long long x = p.kv.bt ? (blk < 0 ? -1ll : (long long)blk * p.kv.rpb + (e - (int)(div_by(e, p.kv.div) * p.kv.div.d)))
+        const int in_block = e - (int)(div_by(e, p.kv.div) * p.kv.div.d);
+        long long x = p.kv.bt ? (blk < 0 ? -1ll : (long long)blk * p.kv.rpb + in_block)
                               : (e < p.kv.seq_rows ? r.req * p.kv.seq_rows + e : -1ll);
         if (x >= p.kv.n_rows) x = -1;
         if (p.check && x < 0) atomicOr(&g_mqa_fp4_error, kIdxBlock << 1);
@@ -755,15 +777,18 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       // The codes of this thread's group of block b of cache row x, in the order of its stores (halves swapped in the
       // second chunk).
       auto fetch = [&](int x, int b) -> uint4 {
-        const uint4 v = x >= 0 && 4 * b + sub < n_groups ? *reinterpret_cast<const uint4*>(codes + x * p.kv.ld_codes + b * 64)
-                                                         : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = x >= 0 && 4 * b + sub < n_groups
+                            ? *reinterpret_cast<const uint4*>(codes + x * p.kv.ld_codes + b * 64)
+                            : make_uint4(0u, 0u, 0u, 0u);
         return chunk ? make_uint4(v.z, v.w, v.x, v.y) : v;
       };
       auto fetch_scales = [&](int x) -> uint4 {
         return x >= 0 ? *reinterpret_cast<const uint4*>(scales + x * p.kv.ld_scales) : make_uint4(0u, 0u, 0u, 0u);
       };
       // This thread's row of chunk c of tile i.
-      auto row_of = [&](int i, int c) -> unsigned char* { return kv + c * kKvChunk + (c == 7 && (i & 1) ? kR2Delta : 0u); };
+      auto row_of = [&](int i, int c) -> unsigned char* {
+        return kv + c * kKvChunk + (c == 7 && (i & 1) ? kR2Delta : 0u);
+      };
       // Copies a quarter of a 128-byte row of chunk c (units 2 sub and 2 sub + 1); zeros where there is none.
       auto copy_row = [&](int i, int c, const bf16* src, bool ok) {
         const uint32_t dst = tc::smem_u32(row_of(i, c));
