@@ -17,9 +17,9 @@
 // so that its fraction is good to 2^-52 at any position and the sine and cosine need no long reduction.
 // Bound: by HBM only where rows are converted as they are (c*4 B in, 366 B out for FP4 at c = 512); with normalisation
 // and rotation by issue slots, 780 instructions a row at 0.6 a cycle and scheduler.  Measured, c = 512: 16,384 f32 rows
-// normalised to FP4 25.7 us (8.6 us of HBM time), 3,001 to FP8 in 13 ragged requests 7.3 us, 256 bf16 rows into rings
-// 2.0 us, 8 rows 4.5 us: a row's chain of loads, f64 sum, inverse root and sine.  An f32 normalisation with error
-// bounds and f64 behind it for every fifth row had as many instructions and took 28 us for the 16,384.
+// normalised to FP4 19.5 us (6.0 us of HBM time; 7.5 us for the loads alone), 3,001 to FP8 in 13 ragged requests 7.4 us,
+// 256 bf16 rows into rings 2.1 us, 8 rows 4.0 us: a row's chain of loads, f64 sum, inverse root and sine.  An f32
+// normalisation with error bounds and f64 behind it for every fifth row took 2 us longer for the 16,384.
 //
 // kv_gather_kernel.  The bf16 values of rows.  Each row is a chain of dependent loads (index, block table, row): a block
 // resolves 32 rows at a time, one a thread, while its warps move the 32 before, four rows in flight per warp (their
@@ -125,7 +125,8 @@ template <bool XF>
 using TurnsOf = std::conditional_t<XF, Turns, NoTurns>;
 
 // Resident blocks per SM that the registers are held to.  Normalised, bf16 form: 7 against 6 took 6.3 against 6.9 us for
-// 4,100 rows; FP8 and FP4, which need a few registers more: 6 against 7 took 25.7 against 26.1 us for 16,384 FP4 rows.
+// 4,100 rows; FP8 and FP4, which need a few registers more: 6 against 7 took 25.7 against 26.1 us for 16,384 FP4 rows and
+// their read-back.
 constexpr int append_blocks(int form, bool xf) {
   return xf ? (form == HCA_KV_BF16 ? 7 : 6) : form == HCA_KV_FP8 ? 8 : 10;
 }

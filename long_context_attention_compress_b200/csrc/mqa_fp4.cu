@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
 // Where few heads would leave columns empty, they are given to neighbouring queries (see Group below).
 //
 // Measured at 64 heads: 8 requests x 8,192 entries 33.6 us, 32 x 1,024 selected 29.3 us; 16 heads, 2 x 192 queries over
-// 8,192 entries 101 us (284 us with a query a CTA).  Steady state, 6.8 k cycles a tile: softmax 2.3 k (S seen to P
+// 2,900 entries 101 us (284 us with a query a CTA).  Steady state, 6.8 k cycles a tile: softmax 2.3 k (S seen to P
 // signalled, beside the next tile's widening), PV 1.55 k (32 MMAs at 48 cycles: each reads 6 KiB of shared memory), the
 // blocks' refill 2.4 k past PV's end (128 KiB of stores beside the 192 KiB that QK^T reads), QK^T's tail 0.5 k.  Around
 // it 11.5 k cycles before the first P (set-up, the chain q_pos - block table - codes, one tile's widening) and 5 k for
