@@ -22,9 +22,11 @@
 // normalisation with error bounds and f64 behind it for every fifth row took 2 us longer for the 16,384.
 //
 // kv_gather_kernel.  The bf16 values of rows.  Each row is a chain of dependent loads (index, block table, row): a block
-// resolves 32 rows at a time, one a thread, while its warps move the 32 before, four rows in flight per warp (their
-// loads predicated, not branched around, so that they issue together).  Bound by memory: 8 x 8,191 FP4 rows 19.3 us
-// (4.7 TB/s read and written; 13.9 us at the copy rate), 32 x 1,024 selected FP8 rows 11.1 us (4.8 TB/s).
+// resolves 16 rows at a time, one a thread, while its warps move the 16 before, two rows in flight per warp (their
+// loads predicated, not branched around, so that they issue together); rows of at most 128 channels take half a warp,
+// four in flight (24,577 rows of 128 FP4 channels 4.0 us, a warp a row 6.3).  Bound by memory: 8 x 8,191 FP4 rows 18.3 us
+// (5.0 TB/s read and written; 13.9 us at the copy rate), 32 x 1,024 selected FP8 rows 10.3 us (5.2 TB/s); with four rows
+// a warp and three blocks an SM 18.9 and 10.7, with two and six 18.5 and 11.4.
 
 #include <cuda_fp16.h>
 
@@ -383,19 +385,22 @@ __device__ __forceinline__ uint32_t load1_if(const void* p, bool ok) {
   return v;
 }
 
-constexpr int kGatherRows = 4;                       // rows in flight per warp
-constexpr int kGatherBlock = 8 * kGatherRows;        // rows a block takes at a time
-constexpr int kGatherResident = 3;                   // blocks per SM
+constexpr int kGatherResident = 5;  // blocks per SM
+// Rows in flight per group of LANES lanes, and rows that a block (8 warps) takes at a time.
+constexpr int gather_rows(int lanes) { return lanes == 32 ? 2 : 4; }
+constexpr int gather_block(int lanes) { return 8 * gather_rows(lanes) * (32 / lanes); }
 
-template <int FORM>
+template <int FORM, int LANES>
 __global__ void __launch_bounds__(256, kGatherResident)
     kv_gather_kernel(KvCache k, FastDiv n_out, uint32_t total, const int32_t* __restrict__ idx,
                      const int32_t* __restrict__ first, bf16* __restrict__ out, long long ld_out, long long seq_out) {
-  __shared__ long long s_row[2][kGatherBlock], s_dst[2][kGatherBlock];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kU = LANES == 32 ? kKvChunks : 1;  // chunks per lane
+  constexpr int kRows = gather_rows(LANES), kBlock = gather_block(LANES), kStep = 32 / LANES;
+  __shared__ long long s_row[2][kBlock], s_dst[2][kBlock];
+  const int lane = threadIdx.x & (LANES - 1);
   const int nch = k.c >> 3;
   const int rope0 = k.c - k.rope_dims;
-  // Where row o comes from and goes to: one row a thread, 32 dependent chains side by side.
+  // Where row o comes from and goes to: one row a thread, 16 dependent chains side by side.
   auto resolve = [&](uint32_t o, int buf) {
     const int b = (int)div_by(o, n_out), j = (int)(o - b * n_out.d);
     int e = j;
@@ -408,26 +413,26 @@ __global__ void __launch_bounds__(256, kGatherResident)
     s_row[buf][threadIdx.x] = kv_row(k, b, e);
     s_dst[buf][threadIdx.x] = b * seq_out + j * ld_out;
   };
-  const uint32_t stride = gridDim.x * kGatherBlock;
-  uint32_t base = blockIdx.x * kGatherBlock;
-  if (threadIdx.x < kGatherBlock && base + threadIdx.x < total) resolve(base + threadIdx.x, 0);
+  const uint32_t stride = gridDim.x * kBlock;
+  uint32_t base = blockIdx.x * kBlock;
+  if (threadIdx.x < kBlock && base + threadIdx.x < total) resolve(base + threadIdx.x, 0);
   __syncthreads();
   for (int buf = 0; base < total; base += stride, buf ^= 1) {
     // (total < 2^31 and the stride is a few thousand rows a time: no overflow)
-    if (threadIdx.x < kGatherBlock && base + stride + threadIdx.x < total) resolve(base + stride + threadIdx.x, buf ^ 1);
+    if (threadIdx.x < kBlock && base + stride + threadIdx.x < total) resolve(base + stride + threadIdx.x, buf ^ 1);
     {
-      const int s0 = warp * kGatherRows;
-      long long row[kGatherRows];
-      uint4 raw[kKvChunks][kGatherRows];
-      uint32_t sc[kKvChunks][kGatherRows];
+      const int s0 = (threadIdx.x >> 5) * kRows * kStep + ((threadIdx.x & 31) / LANES);
+      long long row[kRows];
+      uint4 raw[kU][kRows];
+      uint32_t sc[kU][kRows];
 #pragma unroll
-      for (int r = 0; r < kGatherRows; ++r) row[r] = base + s0 + r < total ? s_row[buf][s0 + r] : -1;
+      for (int r = 0; r < kRows; ++r) row[r] = base + s0 + r * kStep < total ? s_row[buf][s0 + r * kStep] : -1;
 #pragma unroll
-      for (int u = 0; u < kKvChunks; ++u) {
+      for (int u = 0; u < kU; ++u) {
         const int ch = lane + 32 * u, d = ch * 8;
         const bool wide = FORM == HCA_KV_BF16 || d >= rope0;
 #pragma unroll
-        for (int r = 0; r < kGatherRows; ++r) {
+        for (int r = 0; r < kRows; ++r) {
           const bool ok = row[r] >= 0 && ch < nch;
           const uint8_t* code = reinterpret_cast<const uint8_t*>(k.codes);
           if constexpr (FORM == HCA_KV_BF16) {
@@ -448,12 +453,12 @@ __global__ void __launch_bounds__(256, kGatherResident)
         }
       }
 #pragma unroll
-      for (int u = 0; u < kKvChunks; ++u) {
+      for (int u = 0; u < kU; ++u) {
         const int ch = lane + 32 * u, d = ch * 8;
         const bool wide = FORM == HCA_KV_BF16 || d >= rope0;
 #pragma unroll
-        for (int r = 0; r < kGatherRows; ++r) {
-          if (base + s0 + r >= total || ch >= nch) continue;
+        for (int r = 0; r < kRows; ++r) {
+          if (base + s0 + r * kStep >= total || ch >= nch) continue;
           uint4 w = raw[u][r];
           if (!wide && row[r] >= 0) {
             if constexpr (FORM == HCA_KV_FP8) {
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(256, kGatherResident)
               w = e2m1x8_times(raw[u][r].x, e8m0_bf16x2(sc[u][r]));
             }
           }
-          *reinterpret_cast<uint4*>(out + s_dst[buf][s0 + r] + d) = w;
+          *reinterpret_cast<uint4*>(out + s_dst[buf][s0 + r * kStep] + d) = w;
         }
       }
     }
@@ -520,20 +525,30 @@ cudaError_t launch_kv_append(const KvAppend& a, const KvCache& k, cudaStream_t s
   return cudaGetLastError();
 }
 
+template <int FORM>
+static void gather_rows_of(const KvCache& k, int n_out, long long total, const int32_t* idx, const int32_t* first,
+                           bf16* out, long long ld_out, long long seq_out, cudaStream_t stream) {
+  const bool narrow = k.c <= 128;  // half a warp a row
+  const int block = gather_block(narrow ? 16 : 32);
+  const unsigned grid =
+      (unsigned)std::min<long long>((total + block - 1) / block, (long long)kGatherResident * device_sm_count());
+  const FastDiv n = fast_div((uint32_t)n_out);
+  if (narrow)
+    kv_gather_kernel<FORM, 16><<<grid, 256, 0, stream>>>(k, n, (uint32_t)total, idx, first, out, ld_out, seq_out);
+  else
+    kv_gather_kernel<FORM, 32><<<grid, 256, 0, stream>>>(k, n, (uint32_t)total, idx, first, out, ld_out, seq_out);
+}
+
 cudaError_t launch_kv_gather(const KvCache& k, int B, int n_out, const int32_t* idx, const int32_t* first, bf16* out,
                              long long ld_out, long long seq_out, cudaStream_t stream) {
   const long long total = (long long)B * n_out;
   if (total <= 0) return cudaSuccess;
-  const unsigned grid = (unsigned)std::min<long long>((total + kGatherBlock - 1) / kGatherBlock,
-                                                      (long long)kGatherResident * device_sm_count());
-  const FastDiv n = fast_div((uint32_t)n_out);
-  const uint32_t rows = (uint32_t)total;
   if (k.form == HCA_KV_BF16)
-    kv_gather_kernel<HCA_KV_BF16><<<grid, 256, 0, stream>>>(k, n, rows, idx, first, out, ld_out, seq_out);
+    gather_rows_of<HCA_KV_BF16>(k, n_out, total, idx, first, out, ld_out, seq_out, stream);
   else if (k.form == HCA_KV_FP8)
-    kv_gather_kernel<HCA_KV_FP8><<<grid, 256, 0, stream>>>(k, n, rows, idx, first, out, ld_out, seq_out);
+    gather_rows_of<HCA_KV_FP8>(k, n_out, total, idx, first, out, ld_out, seq_out, stream);
   else
-    kv_gather_kernel<HCA_KV_FP4><<<grid, 256, 0, stream>>>(k, n, rows, idx, first, out, ld_out, seq_out);
+    gather_rows_of<HCA_KV_FP4>(k, n_out, total, idx, first, out, ld_out, seq_out, stream);
   ++g_launch_counter;
   return cudaGetLastError();
 }

@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
 // blocks' refill 2.4 k past PV's end (128 KiB of stores beside the 192 KiB that QK^T reads), QK^T's tail 0.5 k.  Around
 // it 11.5 k cycles before the first P (set-up, the chain q_pos - block table - codes, one tile's widening) and 5 k for
 // 128 KiB of partial states (26 B a cycle and SM, the rate of L2 writes), then the combine.
-// Tried and dropped: QK^T from rows in TMEM with V's stores behind PV (the converters' work comes in series: 45 us);
-// one proxy fence for several blocks, the widening held back until P is signalled, the E2M1 conversion instruction for
+// Tried and dropped: QK^T from rows in TMEM with V's stores behind PV (the converters' work comes in series, or their
+// loads touch 32 rows each: 45 and 37.5 us); one proxy fence for several blocks, the widening held back until P is signalled, the E2M1 conversion instruction for
 // half of the codes (no gain or slower).
 constexpr int kSoft = 8, kConv = 16;
 constexpr int kThreads = 32 * (4 + kSoft + kConv);   // whole warpgroups, for the register split

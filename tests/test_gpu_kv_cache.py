@@ -189,7 +189,8 @@ def test_rows_without_a_place_are_left_out():
 
 
 @pytest.mark.parametrize("form", FORMS)
-@pytest.mark.parametrize("c,rope,rpb,spread", [(512, 64, 32, 0), (512, 0, 0, 1), (128, 0, 5, 0), (320, 128, 1, 2)])
+@pytest.mark.parametrize("c,rope,rpb,spread", [(512, 64, 32, 0), (512, 0, 0, 1), (128, 0, 5, 0), (320, 128, 1, 2),
+                                               (64, 0, 3, 0), (128, 64, 0, 1)])
 def test_gather(form, c, rope, rpb, spread):
     """Chosen, consecutive and leading entries; negative and absent ones read as zeros."""
     import long_context_attention_compress_b200 as hca
