@@ -319,3 +319,22 @@ def test_values_that_are_not_finite():
             assert torch.isfinite(y[0, 6:]).all()
         else:
             assert torch.isfinite(y[0, :448]).all() and torch.isfinite(y[1, :64]).all()
+
+
+def test_output_on_another_stream_takes_no_memory_in_use():
+    """A call given another stream makes its output there: a block that the current stream has freed, but still reads,
+    is not written over."""
+    import long_context_attention_compress_b200 as hca
+    k = Cache("bf16", 512, 0, 4, 64)
+    for _ in range(2):
+        x = torch.full((4, 64, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = torch.empty_like(x)
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)  # (some ten milliseconds)
+        y.copy_(x)
+        del x
+        out = hca.kv_cache_gather(k.handle, 4, 64, stream=st)
+        torch.cuda.synchronize()
+        assert (y == 7).all()
+        assert torch.equal(out, hca.kv_cache_gather(k.handle, 4, 64))
