@@ -16,8 +16,8 @@
 // The angle is formed in turns from theta / 2 pi in two f64 words (a table made on the host) with an error-free product,
 // so that its fraction is good to 2^-52 at any position and the sine and cosine need no long reduction.
 // Bound: by HBM only where rows are converted as they are (c*4 B in, 366 B out for FP4 at c = 512); with normalisation
-// and rotation by issue slots, 780 instructions a row at 0.6 a cycle and scheduler.  Measured, c = 512: 16,384 f32 rows
-// normalised to FP4 19.5 us (6.0 us of HBM time; 7.5 us for the loads alone), 3,001 to FP8 in 13 ragged requests 7.4 us,
+// and rotation by issue slots, 760 instructions a row at 0.6 a cycle and scheduler.  Measured, c = 512: 16,384 f32 rows
+// normalised to FP4 19.1 us (6.0 us of HBM time; 7.5 us for the loads alone), 3,001 to FP8 in 13 ragged requests 7.4 us,
 // 256 bf16 rows into rings 2.1 us, 8 rows 4.0 us: a row's chain of loads, f64 sum, inverse root and sine.  An f32
 // normalisation with error bounds and f64 behind it for every fifth row took 2 us longer for the 16,384.
 //
@@ -115,6 +115,16 @@ __device__ __forceinline__ uint2 e4m3x8_encode(const float* y, float sc) {
     if (t < 4) r.x = (r.x & ~(255u << sh)) | (c << sh);
     else r.y = (r.y & ~(255u << sh)) | (c << sh);
   }
+  return r;
+}
+
+// Two f32 products in one instruction (16,384 normalised rows 19.7 -> 19.1 us).
+__device__ __forceinline__ float2 mul2(float a0, float a1, float b0, float b1) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
   return r;
 }
 
@@ -273,9 +283,10 @@ __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
           uint32_t w[4], differ = 0;
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const float y0 = v[u][2 * t] * g[2 * t], y1 = v[u][2 * t + 1] * g[2 * t + 1];
-            w[t] = pack_bf16x2(y0 * inv_lo, y1 * inv_lo);
-            differ |= w[t] ^ pack_bf16x2(y0 * inv_hi, y1 * inv_hi);
+            const float2 y = mul2(v[u][2 * t], v[u][2 * t + 1], g[2 * t], g[2 * t + 1]);
+            const float2 lo = mul2(y.x, y.y, inv_lo, inv_lo), hi = mul2(y.x, y.y, inv_hi, inv_hi);
+            w[t] = pack_bf16x2(lo.x, lo.y);
+            differ |= w[t] ^ pack_bf16x2(hi.x, hi.y);
           }
           if (differ) {
 #pragma unroll
@@ -330,7 +341,11 @@ __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
         const float down = __uint_as_float(sb < 254u ? (254u - sb) << 23 : 0x00400000u);
         float y[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) y[t] = v[u][t] * down;
+        for (int t = 0; t < 8; t += 2) {
+          const float2 s = mul2(v[u][t], v[u][t + 1], down, down);
+          y[t] = s.x;
+          y[t + 1] = s.y;
+        }
         *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(k.codes) + row * k.ld_codes + d / 2) =
             e2m1x8_encode(y);
         if ((ch & 3) == 0) reinterpret_cast<uint8_t*>(k.scales)[row * k.ld_scales + ch / 4] = (uint8_t)sb;
