@@ -47,7 +47,8 @@
  *     entries and entries without a row.
  *   - Every entry point that launches work opens an NVTX range named after
  *     itself for the duration of the host call (no cost without a tool).
- *   - Supported shapes: c in {64, 512}, d_idx in {32, 128}; n_heads,
+ *   - Supported shapes (the KV cache calls state their own): c in {64, 512},
+ *     d_idx in {32, 128}; n_heads,
  *     n_idx_heads <= 64; topk <= 2048; n_win <= 256.  Other shapes return
  *     HCA_ERR_UNSUPPORTED.
  */
