@@ -426,7 +426,8 @@ typedef struct {
  *   has fewer than 2^31 rows.  out overlaps no input.  A row that is not finite
  *   reaches the queries that see it and no other.  The entries are widened on chip (exactly) and
  *   multiplied in bf16; logits, softmax and sums are f32, and the probabilities
- *   enter the second product rounded to bf16, as the sum they are divided by.
+ *   enter the second product as the sum of two bf16 terms (within 2^-15 of them), as
+ *   does the sum they are divided by.
  *   ws: sparse_mqa_attend_fp4_workspace(cfg, Tq, N, n_idx) bytes (n_idx = 0
  *   without idx) for the current device; (size_t)-1 for an unsupported shape. */
 int kv_cache_append(const void* x, int x_is_f32, long long ld_x, int n_rows, const int32_t* row_start,

@@ -9,9 +9,9 @@
 // once widened.  Widening is what the two do not show: 14 half-rate byte permutes and 4 multiplies per 8 codes, 1.8 k
 // cycles of an SM's four ALUs per 128 rows, against 0.9 k for the flops at full rate.
 // Roundings: products are exact in f32 and summed in f32 by the tensor cores; logits, softmax, states and sums are f32.
-// P is rounded to bf16 for the second product, and the row sums are those of the rounded P, so a common rounding of
-// all weights cancels; the weights' own roundings (2^-9 on average) come to 2e-3 of the output, where its rounding to
-// bf16 alone is 1.7e-3.
+// P enters the second product as P_hi + P_lo, P_hi truncated to bf16 and P_lo the rest rounded to bf16 (within 2^-15 of
+// P), and the row sums are those of what is multiplied: the output's rounding to bf16 (1.7e-3) is the only one that
+// shows.  P_hi alone left 2.2e-3.
 
 #include <cudaTypedefs.h>
 
@@ -64,7 +64,7 @@ __device__ __forceinline__ const bf16* window_row(const MqaFp4Problem& p, const 
 // ---- CUDA cores: c other than 512 ------------------------------------------------------
 // One CTA per (query, group of kSH heads, split): rows are widened into shared memory 16 at a time, an online softmax
 // runs over them, and the state (m, l, o) goes to the combine kernel.  Bound by f32 FMAs and shared memory: it took
-// 1.2 ms for the 8 x 8,192 entries of c = 512 that take 33.6 us below; the small widths it serves are short.
+// 1.2 ms for the 8 x 8,192 entries of c = 512 that take 36.5 us below; the small widths it serves are short.
 constexpr int kSThreads = 256, kSRows = 16, kSH = 4;
 
 __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem p, int splits, int rows_per_split,
@@ -175,28 +175,28 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
 // a 128-row tile, widened to bf16 in shared memory (128B-swizzled, eight 64-channel chunks), is the K-major A operand
 // of S^T = R . Q^T and, read MN-major, the A operand of O^T += V^T . P^T.  It is tracked as four 128-channel blocks:
 // PV releases them one by one, the converters refill them with the next tile, and QK^T of that tile follows block by
-// block.  The last chunk has two buffers that tiles use in turn, so that the usual 64 rotary channels are copied a
-// tile ahead.
+// block.
 //   warp 0        MMA issuer (and TMEM owner); warps 1-3 only complete its warpgroup
-//   warps 4-11    softmax: two per TMEM lane quarter (32 rows), 32 heads each; P = 2^(s - m) rounded to bf16, the
-//                 row sums in f32 from the rounded values, formed after P has been handed over; accumulators
-//                 rescaled only when some head's maximum grows by more than 2^8
+//   warps 4-11    softmax: two per TMEM lane quarter (32 rows), 32 heads each; P = 2^(s - m) as two bf16 terms,
+//                 the row sums in f32 from those, formed after P has been handed over; accumulators rescaled only
+//                 when some score exceeds its head's running reference by 20 (in log2)
 //   warps 12-27   converters: eight rows a warp, thread = (row, one of a block's four 32-channel groups), so that a
 //                 warp's load touches eight rows' lines, not 32; the next tile's codes are loaded and widened into
 //                 registers while QK^T and the softmax run, so that only stores lie between PV releasing a block
-//                 and the next QK^T over it; rotary channels and window rows are copied with
-//                 16-byte cp.async
+//                 and the next QK^T over it; rotary channels go the same way without widening (their lines are
+//                 brought to L2 a tile ahead), window rows are copied with 16-byte cp.async
 // Where few heads would leave columns empty, they are given to neighbouring queries (see Group below).
 //
-// Measured at 64 heads: 8 requests x 8,192 entries 33.6 us, 32 x 1,024 selected 29.3 us; 16 heads, 2 x 192 queries over
-// 2,900 entries 101 us (284 us with a query a CTA).  Steady state, 6.8 k cycles a tile: softmax 2.3 k (S seen to P
-// signalled, beside the next tile's widening), PV 1.55 k (32 MMAs at 48 cycles: each reads 6 KiB of shared memory), the
-// blocks' refill 2.4 k past PV's end (128 KiB of stores beside the 192 KiB that QK^T reads), QK^T's tail 0.5 k.  Around
-// it 11.5 k cycles before the first P (set-up, the chain q_pos - block table - codes, one tile's widening) and 5 k for
-// 128 KiB of partial states (26 B a cycle and SM, the rate of L2 writes), then the combine.
+// Measured at 64 heads: 8 requests x 8,192 entries 36.5 us, 32 x 1,024 selected 31.5 us; 16 heads, 2 x 192 queries over
+// 2,900 entries 112 us.  With P as one bf16 term they took 33.6, 29.3 and 101 us, and the outputs were off by a third
+// more than their own rounding.  Steady state, every SM at work: 8.8 k cycles a tile (7.3 k with one term): the softmax,
+// then PV (2.3 k: 288 KiB of operands at the shared-memory rate), the blocks' refill (128 KiB of stores) beside PV's end
+// and QK^T (192 KiB).  Around it 11.5 k cycles before the first P (set-up, the chain q_pos - block table - codes, one
+// tile's widening) and 5 k for 128 KiB of partial states (26 B a cycle and SM, the rate of L2 writes), then the combine.
 // Tried and dropped: QK^T from rows in TMEM with V's stores behind PV (the converters' work comes in series, or their
-// loads touch 32 rows each: 45 and 37.5 us); one proxy fence for several blocks, the widening held back until P is signalled, the E2M1 conversion instruction for
-// half of the codes (no gain or slower).
+// loads touch 32 rows each: 45 and 37.5 us where this took 33.6); one proxy fence for several blocks, the widening held
+// back until P is signalled, the E2M1 conversion instruction for half of the codes, all four blocks widened ahead (no
+// gain or slower).
 constexpr int kSoft = 8, kConv = 16;
 constexpr int kThreads = 32 * (4 + kSoft + kConv);   // whole warpgroups, for the register split
 constexpr int kRowsT = 128;                          // rows per tile
@@ -205,10 +205,10 @@ constexpr int kBlocks = 4;                           // 128-channel blocks of a 
 constexpr uint32_t kQChunk = kHT * 128;              // 8 KiB: 64 channels of the queries
 constexpr uint32_t kKvChunk = kRowsT * 128;          // 16 KiB: 64 channels of the tile
 constexpr uint32_t kQBytes = 8 * kQChunk, kKvBytes = 8 * kKvChunk, kPBytes = kRowsT * kHT * 2;
-constexpr uint32_t kOffQ = 0, kOffKv = kQBytes, kOffP = kOffKv + kKvBytes, kOffR2 = kOffP + kPBytes;
-constexpr uint32_t kOffBars = kOffR2 + kKvChunk;
-constexpr uint32_t kR2Delta = kOffR2 - (kOffKv + 7 * kKvChunk);  // second buffer of the last chunk, after the first
-constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
+constexpr uint32_t kOffQ = 0, kOffKv = kQBytes, kOffP = kOffKv + kKvBytes, kOffBars = kOffP + 2 * kPBytes;
+// TMEM: S^T, then O^T block by block.  Blocks 0-2 keep the products with P_hi and P_lo apart (128 columns: one N = 128
+// MMA reads the rows once for both); the last block, whose 64 columns are what is left, takes them one after the other.
+constexpr uint32_t kColS = 0, kColO = 64, kColBlock = 2 * kHT, kTmemCols = 512;
 constexpr float kRescaleLog2 = 20.f;
 constexpr float kNoMax = -1e30f;                      // running maximum of a head without a score yet
 constexpr int kHpt = kHT * 4 / kSoft;                // heads per softmax thread (32)
@@ -385,8 +385,16 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
   auto store_part = [&](int b, int x, float rc, float rs) {
     uint32_t v[16];
     if (nt > 0) {
-      tc::tmem_ld16(tmem + lanebase + kColO + b * kHT + 16 * x, v);
-      tc::tmem_ld_wait();
+      tc::tmem_ld16(tmem + lanebase + kColO + b * kColBlock + 16 * x, v);
+      if (b < kBlocks - 1) {
+        uint32_t lo[16];
+        tc::tmem_ld16(tmem + lanebase + kColO + b * kColBlock + kHT + 16 * x, lo);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < 16; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) + __uint_as_float(lo[h]));
+      } else {
+        tc::tmem_ld_wait();
+      }
     } else {
 #pragma unroll
       for (int h = 0; h < 16; ++h) v[h] = 0u;
@@ -444,11 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       __syncwarp();
       constexpr uint32_t id_qk = tc::idesc_bf16_f32(kRowsT, kHT, false, false);
       constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, kHT, true, true);
+      constexpr uint32_t id_pv2 = tc::idesc_bf16_f32(128, 2 * kHT, true, true);  // B = [P_hi | P_lo]
       const uint64_t q_desc0 = tc::sdesc_sw128(tc::smem_u32(base + kOffQ), 16, 1024);
       const uint64_t k_desc0 = tc::sdesc_sw128(tc::smem_u32(base + kOffKv), 16, 1024);
       const uint64_t v_desc0 = tc::sdesc_sw128(tc::smem_u32(base + kOffKv), kKvChunk, 1024);
-      // the last block with the second buffer of the last chunk
-      const uint64_t v_desc3 = tc::sdesc_sw128(tc::smem_u32(base + kOffKv + 6 * kKvChunk), kKvChunk + kR2Delta, 1024);
       const uint64_t p_desc0 = tc::sdesc_sw128(tc::smem_u32(base + kOffP), kPBytes, 1024);
       bool ok = tc::warp_wait(&bars->qfull, 0, abort);
       for (int i = 0; ok && i < nt; ++i) {
@@ -459,13 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
           if (!(ok = tc::warp_wait(&bars->vfull[b], ph, abort))) break;
           tc::fence_after_sync();
           const uint64_t kd = k_desc0 + b * (2 * kKvChunk >> 4), qd = q_desc0 + b * (2 * kQChunk >> 4);
-          const uint64_t kd2 = kd + ((kKvChunk + (b == kBlocks - 1 && ph ? kR2Delta : 0u)) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc::mma_bf16_lead(lead, tmem + kColS, kd + 2 * k, qd + 2 * k, id_qk, b + k > 0 ? 1u : 0u);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_lead(lead, tmem + kColS, kd2 + 2 * k, qd + (kQChunk >> 4) + 2 * k, id_qk, 1u);
+            tc::mma_bf16_lead(lead, tmem + kColS, kd + (kKvChunk >> 4) + 2 * k, qd + (kQChunk >> 4) + 2 * k, id_qk, 1u);
         }
         if (!ok) break;
         if (lead) tc::mma_commit(&bars->sfull);
@@ -474,11 +480,21 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
         tc::fence_after_sync();
 #pragma unroll 1
         for (int b = 0; b < kBlocks; ++b) {
-          const uint64_t vd = b == kBlocks - 1 && ph ? v_desc3 : v_desc0 + b * (2 * kKvChunk >> 4);
+          const uint64_t vd = v_desc0 + b * (2 * kKvChunk >> 4);
+          const uint32_t od = tmem + kColO + b * kColBlock;
+          if (b < kBlocks - 1) {
 #pragma unroll
-          for (int kk = 0; kk < kRowsT / 16; ++kk)
-            tc::mma_bf16_lead(lead, tmem + kColO + b * kHT, vd + kk * (2048 >> 4), p_desc0 + kk * (2048 >> 4), id_pv,
-                              i + kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < kRowsT / 16; ++kk)  // (the columns of P_lo are the operand's next 64)
+              tc::mma_bf16_lead(lead, od, vd + kk * (2048 >> 4), p_desc0 + kk * (2048 >> 4), id_pv2,
+                                i + kk > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < kRowsT / 16; ++kk) {
+              tc::mma_bf16_lead(lead, od, vd + kk * (2048 >> 4), p_desc0 + kk * (2048 >> 4), id_pv,
+                                i + kk > 0 ? 1u : 0u);
+              tc::mma_bf16_lead(lead, od, vd + kk * (2048 >> 4), p_desc0 + ((kPBytes + kk * 2048) >> 4), id_pv, 1u);
+            }
+          }
           if (lead) tc::mma_commit(&bars->vempty[b]);  // the converters may refill this block
           __syncwarp();
         }
@@ -515,9 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     // Columns are taken 16 at a time, to keep the registers of a thread few.
     float lw = 0.f;  // lane l: column 32 hsel + l's sum over this warp's rows, relative to the running maximum
     unsigned char* prow = base + kOffP + row * 128;
-    // 128-byte part of this row of tile i in chunk ch.
-    auto row_part = [&](int i, int ch) -> uint4* {
-      return reinterpret_cast<uint4*>(base + kOffKv + ch * kKvChunk + (ch == 7 && (i & 1) ? kR2Delta : 0u) + row * 128);
+    // 128-byte part of this row of the tile in chunk ch.
+    auto row_part = [&](int ch) -> uint4* {
+      return reinterpret_cast<uint4*>(base + kOffKv + ch * kKvChunk + row * 128);
     };
     bool failed = false;
     int i = 0, g = 0;
@@ -571,12 +587,12 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
           if (tc::named_bar_or(1, 32 * kSoft, odd)) {
             if (odd) {
 #pragma unroll 1
-              for (int w = 0; w < 64; ++w) nonfinite |= any_not_finite(row_part(i, w >> 3)[w & 7]);
+              for (int w = 0; w < 64; ++w) nonfinite |= any_not_finite(row_part(w >> 3)[w & 7]);
             }
             tc::named_bar(1, 32 * kSoft);  // (both warps of the quarter have looked)
             if (nonfinite) {
 #pragma unroll 1
-              for (int w = 32 * hsel; w < 32 * hsel + 32; ++w) row_part(i, w >> 3)[w & 7] = make_uint4(0u, 0u, 0u, 0u);
+              for (int w = 32 * hsel; w < 32 * hsel + 32; ++w) row_part(w >> 3)[w & 7] = make_uint4(0u, 0u, 0u, 0u);
             }
           }
         }
@@ -609,13 +625,21 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
             }
 #pragma unroll
             for (int h = 0; h < 16; h += 2) top = fmaxf(top, fmaxf(sv[h], sv[h + 1]));
+            uint32_t wl[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(fast_exp2(sv[2 * k]), fast_exp2(sv[2 * k + 1])) & vmask;
+            for (int k = 0; k < 8; ++k) {
+              const float p0 = fast_exp2(sv[2 * k]), p1 = fast_exp2(sv[2 * k + 1]);
+              const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+              w[k] = prmt_raw(u0, u1, 0x7632u) & vmask;
+              wl[k] = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u), p1 - __uint_as_float(u1 & 0xffff0000u)) & vmask;
+            }
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
               const int c = (kHpt / 8) * hsel + 2 * x + cc;  // 16-byte unit of the row: columns 8c .. 8c+7
-              *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
-                  make_uint4(w[4 * cc], w[4 * cc + 1], w[4 * cc + 2], w[4 * cc + 3]);
+              unsigned char* to = prow + ((c ^ (row & 7)) << 4);
+              *reinterpret_cast<uint4*>(to) = make_uint4(w[4 * cc], w[4 * cc + 1], w[4 * cc + 2], w[4 * cc + 3]);
+              *reinterpret_cast<uint4*>(to + kPBytes) =
+                  make_uint4(wl[4 * cc], wl[4 * cc + 1], wl[4 * cc + 2], wl[4 * cc + 3]);
             }
           }
           return valid ? top : neg_inf();
@@ -671,9 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
             // O^T holds the sums up to tile i-1 (PV(i-1) was issued before QK(i), whose commit has arrived)
             tc::fence_after_sync();
 #pragma unroll 1
-            for (int part = 0; part < kBlocks * (kHpt / 16); ++part) {
+            for (int part = 0; part < (2 * kBlocks - 1) * (kHpt / 16); ++part) {
               const int hh = kHpt * hsel + 16 * (part & 1);
-              const uint32_t ta = tmem + lanebase + kColO + (part >> 1) * kHT + hh;
+              const uint32_t ta = tmem + lanebase + kColO + (part >> 1) * kHT + hh;  // (64 columns of a term each)
               uint32_t v[16];
               tc::tmem_ld16(ta, v);
               tc::tmem_ld_wait();
@@ -696,10 +720,12 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             const int c = (kHpt / 8) * hsel + 2 * x + cc;
-            float f[8];
-            unpack8(*reinterpret_cast<const uint4*>(prow + ((c ^ (row & 7)) << 4)), f);
+            const unsigned char* at = prow + ((c ^ (row & 7)) << 4);
+            float f[8], lo[8];
+            unpack8(*reinterpret_cast<const uint4*>(at), f);
+            unpack8(*reinterpret_cast<const uint4*>(at + kPBytes), lo);
 #pragma unroll
-            for (int h = 0; h < 8; ++h) sv[8 * cc + h] = f[h];
+            for (int h = 0; h < 8; ++h) sv[8 * cc + h] = f[h] + lo[h];
           }
           const float t = warp_sum16(sv, lane);
           if ((lane >> 4) == x) lw += t;
@@ -733,7 +759,6 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     const int cw = warp - 4 - kSoft;
     const int row = 8 * cw + (lane >> 2), sub = lane & 3;    // row of the tile; group 4b + sub of block b
     const int n_groups = (kC - p.kv.rope_dims) / kFp4Group;  // groups held in 4 bits
-    const bool rope64 = p.kv.rope_dims == 64;                // the last chunk is copied a tile ahead
     const uint8_t* codes = reinterpret_cast<const uint8_t*>(p.kv.codes) + sub * 16;
     const uint8_t* scales = reinterpret_cast<const uint8_t*>(p.kv.scales);
     const int chunk = sub >> 1;                              // of a block's two
@@ -785,21 +810,17 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       auto fetch_scales = [&](int x) -> uint4 {
         return x >= 0 ? *reinterpret_cast<const uint4*>(scales + x * p.kv.ld_scales) : make_uint4(0u, 0u, 0u, 0u);
       };
-      // This thread's row of chunk c of tile i.
-      auto row_of = [&](int i, int c) -> unsigned char* {
-        return kv + c * kKvChunk + (c == 7 && (i & 1) ? kR2Delta : 0u);
-      };
       // Copies a quarter of a 128-byte row of chunk c (units 2 sub and 2 sub + 1); zeros where there is none.
-      auto copy_row = [&](int i, int c, const bf16* src, bool ok) {
-        const uint32_t dst = tc::smem_u32(row_of(i, c));
+      auto copy_row = [&](int c, const bf16* src, bool ok) {
+        const uint32_t dst = tc::smem_u32(kv + c * kKvChunk);
 #pragma unroll
         for (uint32_t w = 0; w < 2; ++w)
           tc::cp_async16(dst + (((2 * sub + w) ^ sw) << 4), src + (2 * sub + w) * 8, ok ? 16 : 0);
       };
-      // The 64 rotary channels of cache row x, into the last chunk of tile i.
-      auto copy_rope = [&](int i, int x) {
-        copy_row(i, 7, p.kv.rope + (x >= 0 ? x * p.kv.ld_rope : 0ll), x >= 0);
-        tc::cp_async_commit();
+      // The rotary channels of cache row x on their way to L2.
+      auto fetch_rope = [&](int x) {
+        if (x >= 0 && sub == 0 && p.kv.rope_dims > 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.kv.rope + x * p.kv.ld_rope));
       };
       // An entry's index, its block and its row are dependent loads, each given a tile's time: x is the cache row of the
       // tile being converted, e1 and b1 entry and block of the next one, e2 the entry of the one after.
@@ -807,26 +828,24 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
       int e1 = entry_of(la + 1), e2 = entry_of(la + 2);
       int x = resolve(la, e0, block_of(e0));
       int b1 = block_of(e1);
-      if (rope64 && la < le) copy_rope(i, x);  // (PV of tile i-2 has released this buffer)
-      // Widen this thread's group of block b (one that is not held in 4 bits: its codes are zeros).
+      fetch_rope(x);
+      // This thread's group of block b in bf16, in the order of its stores: widened, or rotary channels as they are.
       auto widen = [&](int b, const uint4& v, uint32_t scale_word, uint4 (&o)[4]) {
-        e2m1x32_to_bf16(v, (scale_word >> (8 * sub)) & 255u, o);
-      };
-      // Store a widened group of block b and signal the block.
-      auto put = [&](int i, int b, const uint4 (&o)[4]) {
         const int g = 4 * b + sub;
-        unsigned char* d = row_of(i, 2 * b + chunk);
         if (g < n_groups) {
+          e2m1x32_to_bf16(v, (scale_word >> (8 * sub)) & 255u, o);
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(p.kv.rope + (x >= 0 ? x * p.kv.ld_rope : 0ll) +
+                                                            (g - n_groups) * 32);
 #pragma unroll
-          for (uint32_t w = 0; w < 4; ++w) *reinterpret_cast<uint4*>(d + (((unit0 ^ w) ^ sw) << 4)) = o[w];
-        } else if (!rope64) {  // other numbers of rotary channels: copied here
-          const bf16* src = p.kv.rope + (x >= 0 ? x * p.kv.ld_rope + (g - n_groups) * 32 : 0ll);
-#pragma unroll 1
-          for (uint32_t w = 0; w < 4; ++w)
-            tc::cp_async16(tc::smem_u32(d) + (((4 * (sub & 1) + w) ^ sw) << 4), src + w * 8, x >= 0 ? 16 : 0);
-          tc::cp_async_commit();
+          for (int w = 0; w < 4; ++w) o[w] = x >= 0 ? src[(2 * chunk) ^ w] : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (b == kBlocks - 1 || !rope64) tc::cp_async_wait<0>();  // (64 rotary channels: under way since the last tile)
+      };
+      // Store such a group and signal the block.
+      auto put = [&](int b, const uint4 (&o)[4]) {
+        unsigned char* d = kv + (2 * b + chunk) * kKvChunk;
+#pragma unroll
+        for (uint32_t w = 0; w < 4; ++w) *reinterpret_cast<uint4*>(d + (((unit0 ^ w) ^ sw) << 4)) = o[w];
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->vfull[b]);
@@ -843,15 +862,14 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
         widen(1, v1, sc.y, ob);
         widen(2, v2, sc.z, oc);
         if (!(okw = tc::warp_wait(&bars->vempty[0], ph ^ 1, abort))) break;
-        put(i, 0, oa);
+        put(0, oa);
         widen(3, v3, sc.w, oa);
         if (!(okw = tc::warp_wait(&bars->vempty[kBlocks - 1], ph ^ 1, abort))) break;
-        put(i, 1, ob);
-        put(i, 2, oc);
-        put(i, 3, oa);
-        // PV of tile i-1 has released its buffer of the last chunk: it takes tile i+1's
+        put(1, ob);
+        put(2, oc);
+        put(3, oa);
         x = resolve(lt + 1, e1, b1);
-        if (rope64 && lt + 1 < le) copy_rope(i + 1, x);
+        fetch_rope(x);
         e1 = e2;
         b1 = block_of(e1);
         e2 = entry_of(lt + 3);
@@ -866,8 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
 #pragma unroll 1
         for (int b = 0; b < kBlocks; ++b) {
           if (!tc::warp_wait(&bars->vempty[b], ph ^ 1, abort)) { okw = false; break; }
-          copy_row(i, 2 * b, src + b * 128, valid);
-          copy_row(i, 2 * b + 1, src + b * 128 + 64, valid);
+          copy_row(2 * b, src + b * 128, valid);
+          copy_row(2 * b + 1, src + b * 128 + 64, valid);
           tc::cp_async_commit();
           if (b > 0) {
             tc::cp_async_wait<1>();
