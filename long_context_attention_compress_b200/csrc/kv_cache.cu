@@ -10,7 +10,7 @@
 // Roundings.  With normalisation or rotation y is rounded to bf16 first (what the bf16 cache holds), as from the
 // float64 value: a quantised code must not depend on which side of a midpoint an f32 normalisation falls.  Sum of
 // squares and rotation are f64; the other channels are formed in f32, 8 ulps too low and too high (f32 is within 4),
-// and redone in f64 only where the two round apart.  The codes are those of the stored-form definitions bit for bit:
+// and redone in f64 only where the two round apart, or where a factor or a product may leave f32's normal range.  The codes are those of the stored-form definitions bit for bit:
 // FP4 scaling is exact and the conversion rounds to nearest even; an f32 quotient (by the reciprocal, within 2 ulps)
 // that is within 4 ulps of an E4M3 midpoint, or in E4M3's subnormal range, is decided on the f64 quotient.
 // The angle is formed in turns from theta / 2 pi in two f64 words (a table made on the host) with an error-free product,
@@ -255,6 +255,10 @@ __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         inv = rsqrt(fma(ss, inv_c, (double)a.eps));
       }
+      // The f32 products below are good to their last bits while nothing overflows or falls to a subnormal: |v| is at most
+      // sqrt(c) / inv < 2^45 for an inv of at least 2^-40, |gamma| below 2^60, and a result of at least 2^-80 had factors
+      // that were normal.
+      const bool narrow = inv >= 0x1p-40 && inv <= 0x1p40;
       const float inv_lo = (float)inv * (1.f - 0x1p-21f), inv_hi = (float)inv * (1.f + 0x1p-21f);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -281,14 +285,17 @@ __global__ void __launch_bounds__(32 * kKvWarps, append_blocks(FORM, XF))
           // The value lies between these two f32 products, 8 ulps apart either way; where both round to one bf16, so
           // does it.
           uint32_t w[4], differ = 0;
+          float least = 1.f, top = 0.f;
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const float2 y = mul2(v[u][2 * t], v[u][2 * t + 1], g[2 * t], g[2 * t + 1]);
             const float2 lo = mul2(y.x, y.y, inv_lo, inv_lo), hi = mul2(y.x, y.y, inv_hi, inv_hi);
             w[t] = pack_bf16x2(lo.x, lo.y);
             differ |= w[t] ^ pack_bf16x2(hi.x, hi.y);
+            least = fminf(least, fminf(fabsf(lo.x), fabsf(lo.y)));
+            top = fmaxf(top, fmaxf(fabsf(g[2 * t]), fabsf(g[2 * t + 1])));
           }
-          if (differ) {
+          if (differ || !narrow || least < 0x1p-80f || top > 0x1p60f) {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
               w[t] = pack_bf16x2((float)((double)v[u][2 * t] * inv * (double)g[2 * t]),

@@ -1,0 +1,52 @@
+"""kv_cache_append and kv_cache_gather at the ends of their range: magnitudes near f32's limits, and launches large enough
+that a warp or a block walks several rows.  Compared as in test_gpu_kv_cache: codes, scales and unrotated bf16 channels bit
+for bit with the oracle's float64 values, rotated channels within a bf16 step."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from kv_cache_util import Cache
+from test_gpu_kv_cache import BASE, FORMS, _check
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device="cuda")
+
+
+def _normed(x, entries, rate, gamma, eps, rope):
+    y = oracle.rms_norm(x.double().numpy(), gamma.double().numpy(), eps)
+    return oracle.round_bf16(oracle.rope(y, (np.asarray(entries, dtype=np.int64) + 1) * rate - 1, rope, BASE))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+@pytest.mark.parametrize("gammas", ["up to 2", "far apart"])
+def test_append_normalises_any_magnitude(form, dtype, eps, gammas):
+    """Rows from f32's subnormals to its largest values, with and without an eps that outweighs them, single channels far
+    below their row's: products that pass f32's range on the way to an ordinary value."""
+    import long_context_attention_compress_b200 as hca
+    rng = np.random.default_rng(1)
+    scales = [3.3e38, 2.6e38, 1e38, 3e37, 1e30, 1e13, 1.0, 1e-13, 1e-30, 1e-37, 1e-38, 1e-40]
+    if dtype is torch.float32:
+        scales.append(1e-43)  # (below bf16's least)
+    x = rng.uniform(0.5, 1.0, size=(2 * len(scales), 512)) * rng.choice([-1.0, 1.0], size=(2 * len(scales), 512))
+    x *= np.repeat(scales, 2)[:, None]
+    x[1::2, ::5] *= 10.0 ** rng.uniform(-45, 0, size=x[1::2, ::5].shape)  # (some become zeros)
+    x = torch.tensor(x).to(dtype)
+    assert torch.isfinite(x).all()
+    gamma = torch.tensor(rng.uniform(0.5, 2.0, 512), dtype=torch.float32)
+    if gammas == "far apart":
+        gamma[::7] *= 2.0 ** 70
+        gamma[3::7] *= 2.0 ** -70
+        gamma[5::49] = 0.0
+    n = len(x)
+    k = Cache(form, 512, 64, 1, n, rpb=8)
+    before = k.bytes()
+    hca.kv_cache_append(x.cuda(), k.handle, _i32([0]), row_start=_i32([0, n]), rate=4, gamma=gamma.cuda(), rotate=True,
+                        norm_eps=eps, rope_base=BASE)
+    _check(k, before, [k.row(0, e) for e in range(n)], _normed(x, np.arange(n), 4, gamma, float(np.float32(eps)), 64), True)
