@@ -130,12 +130,15 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
     }
     __syncthreads();
     if (tid < kSH) {
+      // (the maximum takes no account of a NaN, but its row's weight is one; a maximum of -inf, no row yet or none with a
+      // finite score, leaves weights of 0 and NaN)
       float mn = s_m[tid];
       for (int j = 0; j < kSRows; ++j) mn = fmaxf(mn, s_s[tid][j]);
-      const float alpha = mn == neg_inf() ? 1.f : fast_exp2(s_m[tid] - mn);
+      const float ref = mn == neg_inf() ? 0.f : mn;
+      const float alpha = fast_exp2(s_m[tid] - ref);  // (0 before the first row, whose sums are 0)
       float l = s_l[tid] * alpha;
       for (int j = 0; j < kSRows; ++j) {
-        const float e = mn == neg_inf() ? 0.f : fast_exp2(s_s[tid][j] - mn);
+        const float e = fast_exp2(s_s[tid][j] - ref);
         s_s[tid][j] = e;
         l += e;
       }
