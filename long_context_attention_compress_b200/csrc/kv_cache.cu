@@ -84,6 +84,7 @@ __device__ __forceinline__ bool e4m3_doubtful(float q) {
 // Rounded in f64 to a multiple of E4M3's spacing at its magnitude, ties to even, by adding and taking off 2^52 of them;
 // what is left is a code's value (or past the largest one).
 __device__ __noinline__ uint32_t e4m3_decide(float y, float sc) {
+  if (y == 0.f) return 0u;  // (also of a group so small that its scale is 0)
   const double q = (double)y / (double)sc, a = fabs(q);
   const int e = max((__double2hiint(a) >> 20) - 1023, -6);
   const double big = __hiloint2double((e - 3 + 52 + 1023) << 20, 0);

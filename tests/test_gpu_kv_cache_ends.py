@@ -50,3 +50,36 @@ def test_append_normalises_any_magnitude(form, dtype, eps, gammas):
     hca.kv_cache_append(x.cuda(), k.handle, _i32([0]), row_start=_i32([0, n]), rate=4, gamma=gamma.cuda(), rotate=True,
                         norm_eps=eps, rope_base=BASE)
     _check(k, before, [k.row(0, e) for e in range(n)], _normed(x, np.arange(n), 4, gamma, float(np.float32(eps)), 64), True)
+
+
+def _tiny_rows():
+    """Rows whose largest magnitude is a few of f32's least steps: amax / 448 is 0 in f32 up to 224 of them."""
+    rng = np.random.default_rng(2)
+    steps = rng.integers(-3, 4, size=(6, 512)) * np.array([1, 10, 60, 74, 100, 1000])[:, None]
+    steps[0, :64] = 0
+    return torch.tensor(steps * 2.0 ** -149).float()
+
+
+def _tiny_form(x):
+    """FP8 form of such rows: under a scale of 0 a value that is not 0 takes the largest code of its sign."""
+    y = x[:, :448].double().numpy().reshape(len(x), 7, 64)
+    amax = np.abs(y).max(-1)
+    scale = np.where(amax > 0, amax / 448.0, 1.0).astype(np.float32)
+    q = np.where(scale[..., None] == 0, np.sign(y) * 448.0, y / np.where(scale == 0, 1, scale).astype(np.float64)[..., None])
+    codes = torch.tensor(oracle.round_e4m3(q)).float().to(torch.float8_e4m3fn).view(torch.uint8)
+    return codes.reshape(len(x), 448), torch.tensor(scale)
+
+
+def test_fp8_groups_whose_scale_rounds_to_zero():
+    """Rows converted as they are: the bytes are the form's, and the rows read back as zeros, not as 0 / 0."""
+    import long_context_attention_compress_b200 as hca
+    x = _tiny_rows()
+    k = Cache("fp8", 512, 64, 1, 6)
+    hca.kv_cache_append(x.cuda(), k.handle, _i32([0]), row_start=_i32([0, 6]))
+    codes, scales = _tiny_form(x)
+    assert torch.equal(k.t["scales"][0].cpu(), scales)
+    got = k.t["codes"][0].cpu()
+    assert torch.equal(torch.where(got == 128, 0, got), torch.where(codes == 128, 0, codes))  # (a zero of either sign)
+    back = hca.kv_cache_gather(k.handle, 1, 6)[0].float().cpu()
+    assert (back[:4, :448] == 0).all()  # (up to 222 steps)
+    assert torch.isfinite(back).all()
