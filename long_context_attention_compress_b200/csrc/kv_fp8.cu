@@ -68,7 +68,10 @@ __global__ void __launch_bounds__(256) kv_fp8_quantize_kernel(const void* __rest
     for (int k = 0; k < 4; ++k) {
       uint32_t word = 0;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) word |= e4m3_encode((double)load_x<F32>(x, xr + j0 + j + 4 * k + b) / sd) << (8 * b);
+      for (int b = 0; b < 4; ++b) {
+        const float v = load_x<F32>(x, xr + j0 + j + 4 * k + b);
+        if (v != 0.f) word |= e4m3_encode((double)v / sd) << (8 * b);  // (a group's scale may have rounded to 0)
+      }
       w[k] = word;
     }
     *reinterpret_cast<uint4*>(cp + j) = make_uint4(w[0], w[1], w[2], w[3]);

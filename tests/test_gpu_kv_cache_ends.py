@@ -83,3 +83,32 @@ def test_fp8_groups_whose_scale_rounds_to_zero():
     back = hca.kv_cache_gather(k.handle, 1, 6)[0].float().cpu()
     assert (back[:4, :448] == 0).all()  # (up to 222 steps)
     assert torch.isfinite(back).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_fp8_form_is_one_for_both_calls(dtype):
+    """kv_fp8_quantize writes what kv_cache_append does also for groups whose scale rounds to 0, for NaN (kept) and for
+    infinities (whose group reads as NaN); no value reaches its neighbours' codes."""
+    import long_context_attention_compress_b200 as hca
+    from long_context_attention_compress_b200 import workloads as wl
+    at = [(6, 5), (8, 2), (8, 3), (8, 4), (7, 70), (9, 200)]
+    x = torch.cat([_tiny_rows(), torch.randn(4, 512, generator=torch.Generator().manual_seed(4))]).to(dtype)
+    for r, c in at:
+        x[r, c] = 0.01  # (not its group's largest)
+    good = x.clone()
+    for (r, c), v in zip(at, [float("nan")] * 4 + [float("inf"), -float("inf")]):
+        x[r, c] = v
+    k = Cache("fp8", 512, 64, 1, 10)
+    hca.kv_cache_append(x.cuda(), k.handle, _i32([0]), row_start=_i32([0, 10]))
+    cfg = hca.make_cfg(wl.PRO)
+    got = dict(zip(("codes", "scales", "rope"), hca.kv_fp8_quantize(x.cuda(), cfg)))
+    for name, t in got.items():
+        assert torch.equal(k.t[name][0].contiguous().view(torch.uint8), t.contiguous().view(torch.uint8)), name
+    codes = got["codes"].cpu()
+    assert all(int(codes[r, c]) & 127 == 127 for r, c in at)
+    want = hca.kv_fp8_quantize(good.cuda(), cfg)[0].cpu()
+    same = torch.ones_like(codes, dtype=torch.bool)
+    for r, c in at[:4]:
+        same[r, c] = False
+    same[7, 64:128] = same[9, 192:256] = False
+    assert torch.equal(codes[same], want[same])
