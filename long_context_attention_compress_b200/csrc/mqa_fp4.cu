@@ -16,6 +16,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "formats.cuh"
@@ -64,7 +65,7 @@ __device__ __forceinline__ const bf16* window_row(const MqaFp4Problem& p, const 
 // ---- CUDA cores: c other than 512 ------------------------------------------------------
 // One CTA per (query, group of kSH heads, split): rows are widened into shared memory 16 at a time, an online softmax
 // runs over them, and the state (m, l, o) goes to the combine kernel.  Bound by f32 FMAs and shared memory: it took
-// 1.2 ms for the 8 x 8,192 entries of c = 512 that take 36.5 us below; the small widths it serves are short.
+// 1.2 ms for the 8 x 8,192 entries of c = 512 that take 37.0 us below; the small widths it serves are short.
 constexpr int kSThreads = 256, kSRows = 16, kSH = 4;
 
 __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem p, int splits, int rows_per_split,
@@ -190,8 +191,8 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
 //                 brought to L2 a tile ahead), window rows are copied with 16-byte cp.async
 // Where few heads would leave columns empty, they are given to neighbouring queries (see Group below).
 //
-// Measured at 64 heads: 8 requests x 8,192 entries 36.5 us, 32 x 1,024 selected 31.5 us; 16 heads, 2 x 192 queries over
-// 2,900 entries 112 us.  With P as one bf16 term they took 33.6, 29.3 and 101 us, and the outputs were off by a third
+// Measured at 64 heads: 8 requests x 8,192 entries 37.0 us, 32 x 1,024 selected 31.9 us; 16 heads, 2 x 192 queries over
+// 2,900 entries 113 us.  With P as one bf16 term they took 33.6, 29.3 and 101 us, and the outputs were off by a third
 // more than their own rounding.  Steady state, every SM at work: 8.8 k cycles a tile (7.3 k with one term): the softmax,
 // then PV (2.3 k: 288 KiB of operands at the shared-memory rate), the blocks' refill (128 KiB of stores) beside PV's end
 // and QK^T (192 KiB).  Around it 11.5 k cycles before the first P (set-up, the chain q_pos - block table - codes, one
@@ -213,7 +214,11 @@ constexpr uint32_t kOffQ = 0, kOffKv = kQBytes, kOffP = kOffKv + kKvBytes, kOffB
 // MMA reads the rows once for both); the last block, whose 64 columns are what is left, takes them one after the other.
 constexpr uint32_t kColS = 0, kColO = 64, kColBlock = 2 * kHT, kTmemCols = 512;
 constexpr float kRescaleLog2 = 20.f;
-constexpr float kNoMax = -1e30f;                      // running maximum of a head without a score yet
+constexpr float kNoMax = -3.4028234663852886e38f;     // running maximum of a head without a score yet: f32's least
+// A reference is a scaled score rounded down.  Scaled scores minus their reference are one FMA, whose product is exact:
+// what the reference was rounded by, less than 8 below this magnitude, stays in every weight of the head and cancels.
+// Above it, it could pass the exponential's range: there every product is rounded as the reference was (see write_p).
+constexpr float kLarge = 0x1p27f;
 constexpr int kHpt = kHT * 4 / kSoft;                // heads per softmax thread (32)
 constexpr int kOutLd = kC + 8;                       // staged output row (bf16), padded against bank conflicts
 
@@ -224,7 +229,8 @@ struct __align__(16) Bars {
   uint64_t qfull, vfull[kBlocks], vempty[kBlocks], sfull, pfull, odone, drain;
   uint32_t rowok[4][kConv];  // [tile % 4][converter warp]: bit 4 j is set where row j of the warp's eight takes part
   uint32_t tmem_base;
-  int abort;
+  alignas(8) int abort;
+  int large;             // some head's reference is kLarge or more in magnitude (read together with abort)
 };
 constexpr size_t kSmemBytes = 1024 + kOffBars + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -334,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
   unsigned char* base = tc::smem_align1024(smem_raw);
   Bars* bars = reinterpret_cast<Bars*>(base + kOffBars);
   volatile int* abort = &bars->abort;
+  volatile unsigned long long* abort_or_large = reinterpret_cast<volatile unsigned long long*>(&bars->abort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sp = blockIdx.x % splits;
   const int heads = PACK ? 1 : (p.H + kHT - 1) / kHT;  // groups of 64 heads
@@ -352,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
     tc::mbar_init(&bars->odone, 1);
     tc::mbar_init(&bars->drain, 1);
     bars->abort = 0;
+    bars->large = 0;
     tc::fence_mbar_init();
   }
   for (int h = threadIdx.x; h < kHT; h += kThreads) bars->nref[h] = -kNoMax;
@@ -605,8 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
           tc::tmem_ld_wait();
         };
         // P(i) against the running maxima (PV(i-1), the last reader of the buffer, has completed), zeros in rows that
-        // take no part; returns the largest score (in units of log2) relative to its head's maximum
-        auto write_p = [&]() -> float {
+        // take no part; returns the largest score (in units of log2) relative to its head's maximum.  The first pass takes
+        // references below kLarge for granted.
+        auto write_p = [&](auto first_pass) -> float {
           float top = neg_inf();
 #pragma unroll
           for (int x = 0; x < kHpt / 16; ++x) {
@@ -620,6 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
               sv[4 * c + 1] = fmaf(__uint_as_float(v[4 * c + 1]), scale_log2, m4.y);
               sv[4 * c + 2] = fmaf(__uint_as_float(v[4 * c + 2]), scale_log2, m4.z);
               sv[4 * c + 3] = fmaf(__uint_as_float(v[4 * c + 3]), scale_log2, m4.w);
+            }
+            if constexpr (!decltype(first_pass)::value) {
+#pragma unroll
+              for (int h = 0; h < 16; ++h) {
+                const float m = bars->nref[kHpt * hsel + 16 * x + h];
+                if (fabsf(m) >= kLarge) sv[h] = __fadd_rn(__fmul_rd(__uint_as_float(v[h]), scale_log2), m);
+              }
             }
             if (PACK && masked) {
 #pragma unroll
@@ -658,18 +674,21 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
               if (lane == 0 && valid) {
 #pragma unroll
                 for (int h = 0; h < 16; ++h) {
-                  const float m = __uint_as_float(v[h]) * scale_log2;
-                  if (((sees >> (16 * x + h)) & 1u) && fabsf(m) < -kNoMax) bars->nref[kHpt * hsel + 16 * x + h] = -m;
+                  const float m = __fmul_rd(__uint_as_float(v[h]), scale_log2);
+                  if (((sees >> (16 * x + h)) & 1u) && fabsf(m) <= -kNoMax) {
+                    bars->nref[kHpt * hsel + 16 * x + h] = -m;
+                    if (fabsf(m) >= kLarge) bars->large = 1;
+                  }
                 }
               }
             }
           }
           tc::named_bar(1, 32 * kSoft);
         }
-        const float top = write_p();
-        // One vote for "no score lies above its head's running reference + 20 and nobody failed", the usual case: P
-        // stands.  Otherwise new maxima, rescaled accumulators, and P again.
-        if (tc::named_bar_or(1, 32 * kSoft, top > kRescaleLog2 || failed || *abort)) {
+        const float top = write_p(std::true_type{});
+        // One vote for "no score lies above its head's running reference + 20, no reference is large and nobody failed", the
+        // usual case: P stands.  Otherwise new maxima, rescaled accumulators, and P again.
+        if (tc::named_bar_or(1, 32 * kSoft, top > kRescaleLog2 || failed || *abort_or_large != 0)) {
           if (tc::named_bar_or(1, 32 * kSoft, failed || *abort)) { failed = true; break; }
 #pragma unroll 1
           for (int x = 0; x < kHpt / 16; ++x) {
@@ -679,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
             float m = 0.f;
 #pragma unroll
             for (int h = 0; h < 16; ++h) {
-              const float y = warp_max((ok >> h) & 1u ? __uint_as_float(v[h]) * scale_log2 : neg_inf());
+              const float y = warp_max((ok >> h) & 1u ? __fmul_rd(__uint_as_float(v[h]), scale_log2) : neg_inf());
               if (lane == h) m = y;
             }
             if (lane < 16) bars->red[quarter][kHpt * hsel + 16 * x + lane] = m;
@@ -690,7 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
             const float mo = -bars->nref[st];
             const bool grow = mt > mo + kRescaleLog2;
             bars->alpha[st] = grow ? fast_exp2(mo - mt) : 1.f;
-            if (grow) bars->nref[st] = -mt;
+            if (grow) {
+              bars->nref[st] = -mt;
+              if (fabsf(mt) >= kLarge) bars->large = 1;
+            }
           }
           tc::named_bar(1, 32 * kSoft);
           lw *= bars->alpha[kHpt * hsel + lane];
@@ -710,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
             }
             tc::tmem_st_wait();
           }
-          write_p();
+          write_p(std::false_type{});
         }
         tc::fence_before_sync();
         tc::fence_proxy_async_smem();

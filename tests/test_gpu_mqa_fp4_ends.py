@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from kv_cache_util import fill_rows, values
 from parity_util import to64
 from test_gpu_mqa_fp4 import Setup, check_query
 
@@ -39,3 +40,53 @@ def test_nan_row_among_few(c, rope, H, slots):
     got = to64(s.call(pos, idx=idx))
     assert np.isnan(got[0]).all()
     check_query(got[1], to64(s.q[1]), s.rows(1, 171, 1, 4, idx), s.cfg.scale)
+
+
+@pytest.mark.parametrize("c,rope,H", WIDTHS)
+@pytest.mark.parametrize("n", [1, 5, 300])
+@pytest.mark.parametrize("size", [1e14, 1e16])
+def test_logits_far_below_zero(c, rope, H, n, size):
+    """Logits from -1e29 to -1e36: the least of them takes all the weight, and its row comes out as it is."""
+    s = Setup(c=c, rope=rope, H=H, B=2, N=n, seed=n, win=False)
+    rng = np.random.default_rng(n)
+    y = rng.uniform(0.5, 1.0, size=(2, n, c)) * size * (2.0 + np.arange(n) % 7)[None, :, None]
+    y[:, n // 2] *= 0.25  # (below a half of any other row, channel by channel)
+    rows = to64(torch.tensor(y).bfloat16()).reshape(2 * n, c)
+    fill_rows(s.k, [s.k.row(b, e) for b in range(2) for e in range(n)], rows)
+    s.ref = values("fp4", s.k.bytes(), {m: s.k.width(m) for m in s.k.t}, rope)
+    s.q = -torch.tensor(rng.uniform(0.5, 1.0, size=(2, H, c)) * size).bfloat16()
+    got = to64(s.call([4 * n - 1, 4 * n + 1]))
+    for b in range(2):
+        np.testing.assert_array_equal(got[b], np.broadcast_to(s.ref[s.k.row(b, n // 2)], (H, c)))
+
+
+@pytest.mark.parametrize("H,nq", [(64, 1), (16, 3)])
+@pytest.mark.parametrize("n", [3, 1000])
+@pytest.mark.parametrize("size", [1e2, 1e3, 1e4, 1e5, 1e8])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_large_logits(H, nq, n, size, sign):
+    """Logits of either sign from 1e5 to 1e17, several tiles and splits, one that takes all the weight; ordinary logits for one
+    head among them."""
+    s = Setup(H=H, B=2, N=n, nq=nq, seed=n, win=False, rpb=16)
+    rng = np.random.default_rng(n)
+    y = rng.uniform(0.5, 1.0, size=(2, n, 512)) * size
+    y[:, n // 2] *= 0.25
+    y[:, n // 3] *= 4.0
+    fill_rows(s.k, [s.k.row(b, e) for b in range(2) for e in range(n)], to64(torch.tensor(y).bfloat16()).reshape(2 * n, 512))
+    s.ref = values("fp4", s.k.bytes(), {m: s.k.width(m) for m in s.k.t}, 64)
+    q = rng.uniform(0.5, 1.0, size=(2 * nq, H, 512)) * size * sign
+    q[:, : H // 2] *= -1
+    q[:, 5] /= size * size * 512
+    s.q = torch.tensor(q).bfloat16()
+    pos = np.concatenate([4 * n - 1 + np.arange(nq), 4 * n + 1 + np.arange(nq)])
+    got = to64(s.call(pos, q_req=None if nq == 1 else np.repeat([0, 1], nq)))
+    for i in range(2 * nq):
+        b = i // nq
+        rows = s.rows(i, int(pos[i]), b, 4, None)
+        logits = s.cfg.scale * (to64(s.q[i]) @ rows.T)
+        top = np.sort(logits, 1)
+        clear = top[:, -1] - top[:, -2] > 20 + 2.0 ** -14 * np.abs(top).max(1)  # (told apart by f32 sums of 512 products)
+        clear[5] = False
+        assert clear.sum() >= H // 4
+        np.testing.assert_array_equal(got[i][clear], rows[np.argmax(logits, 1)][clear])
+        check_query(got[i][5:6], to64(s.q[i])[5:6], rows, s.cfg.scale)
