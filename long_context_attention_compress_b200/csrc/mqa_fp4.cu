@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
       const float inv = bars->alpha[16 * x + h];
-      float o = inv != 0.f ? __uint_as_float(v[h]) * inv : 0.f;
+      float o = __uint_as_float(v[h]) * inv;  // (no rows: 0 * 0; rows of weight 0 that are not finite show)
       if (rot) o = fmaf(o, rc, __shfl_xor_sync(0xffffffffu, o, 1) * rs);
       stage[(16 * x + h) * kOutLd + d] = __float2bfloat16_rn(o);
     }

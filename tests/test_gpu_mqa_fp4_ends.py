@@ -90,3 +90,22 @@ def test_large_logits(H, nq, n, size, sign):
         assert clear.sum() >= H // 4
         np.testing.assert_array_equal(got[i][clear], rows[np.argmax(logits, 1)][clear])
         check_query(got[i][5:6], to64(s.q[i])[5:6], rows, s.cfg.scale)
+
+
+@pytest.mark.parametrize("c,rope,H", WIDTHS)
+@pytest.mark.parametrize("n", [1, 3, 200])
+@pytest.mark.parametrize("sink", [False, True])
+def test_only_rows_of_infinities(c, rope, H, n, sink):
+    """Rows whose logits are all -inf (for half of the heads; +inf for the others): no head's output is finite throughout."""
+    s = Setup(c=c, rope=rope, H=H, B=2, N=n, seed=n, win=False)
+    flat = s.k.t["rope"].view(-1, s.k.t["rope"].shape[-1])
+    for e in range(n):
+        flat[s.k.row(0, e), 3] = -INF
+    q = s.q.abs()
+    q[:, ::2] *= -1
+    s.q = q
+    pos = [4 * n - 1, 4 * n]
+    z = np.linspace(-1, 1, H) if sink else None
+    got = to64(s.call(pos, sink=z))
+    assert (~np.isfinite(got[0])).any(axis=1).all()
+    check_query(got[1], to64(s.q[1]), s.rows(1, 4 * n, 1, 4, None), s.cfg.scale, z)
