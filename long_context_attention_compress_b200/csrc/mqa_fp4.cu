@@ -28,6 +28,10 @@ namespace hca {
 __device__ unsigned int g_mqa_fp4_error = 0;
 
 namespace {
+// Entries of N that a query at position t >= 0 sees (t + 1 as an unsigned number: positions go up to 2^31 - 1).
+__device__ __forceinline__ int entries_seen(int t, int rate, int N) {
+  return (int)min(((uint32_t)t + 1u) / (uint32_t)rate, (uint32_t)N);
+}
 // A query's rows: `entries` cache entries (or selected slots), then `window` rows of its request's ring, whose first
 // is the row of token tok0.
 struct Rows {
@@ -41,7 +45,7 @@ __device__ __forceinline__ Rows rows_of(const MqaFp4Problem& p, int q) {
   r.req = p.q_req ? p.q_req[q] : q;
   r.idx = p.idx ? p.idx + (long long)q * p.n_idx : nullptr;
   const bool live = r.t >= 0 && r.req >= 0 && r.req < p.kv.n_req;  // a padding query has no rows
-  r.entries = !live || p.N <= 0 ? 0 : (r.idx ? p.n_idx : n_visible(r.t, p.rate, p.N));
+  r.entries = !live || p.N <= 0 ? 0 : (r.idx ? p.n_idx : entries_seen(r.t, p.rate, p.N));
   r.tok0 = max(0, r.t - p.n_win + 1);
   r.window = live && p.win ? r.t - r.tok0 + 1 : 0;
   return r;
@@ -297,7 +301,7 @@ struct Group {
     req = p.q_req ? p.q_req[q0 + j] : q0 + j;
     idx = p.idx ? p.idx + (long long)q0 * p.n_idx : nullptr;
     if (t < 0 || req < 0 || req >= p.kv.n_req) t = -1;
-    vis = t < 0 || p.N <= 0 ? 0 : (idx ? p.n_idx : n_visible(t, p.rate, p.N));
+    vis = t < 0 || p.N <= 0 ? 0 : (idx ? p.n_idx : entries_seen(t, p.rate, p.N));
     starts = 1u;
     if (PACK) {
       const int t1 = __shfl_up_sync(0xffffffffu, t, 1), r1 = __shfl_up_sync(0xffffffffu, req, 1);
@@ -574,13 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
         uint32_t sees = 0xffffffffu;
         const bool masked = PACK && (r.j1 - r.j0 < grp.n || lt >= r.na || (lt + 1) * kRowsT > r.least);
         if (masked) {
-          const int pos = lt < r.na ? lt * kRowsT + row : r.tok0 + (lt - r.na) * kRowsT + row;
+          const uint32_t pos = lt < r.na ? lt * kRowsT + row : (uint32_t)r.tok0 + (lt - r.na) * kRowsT + row;
           sees = 0u;
 #pragma unroll 1
           for (int c = 0; c < 32; ++c) {
             const int lo = __shfl_sync(0xffffffffu, lt < r.na ? 0 : wlo, c);
             const int n = __shfl_sync(0xffffffffu, lt < r.na ? ecount : wcount, c);
-            if ((unsigned int)(pos - lo) < (unsigned int)n) sees |= 1u << c;
+            if (pos - (uint32_t)lo < (uint32_t)n) sees |= 1u << c;
           }
         }
         // A row with an infinity or a NaN that only some columns see must not reach the others as 0 * NaN: it is zeroed

@@ -109,3 +109,13 @@ def test_only_rows_of_infinities(c, rope, H, n, sink):
     got = to64(s.call(pos, sink=z))
     assert (~np.isfinite(got[0])).any(axis=1).all()
     check_query(got[1], to64(s.q[1]), s.rows(1, 4 * n, 1, 4, None), s.cfg.scale, z)
+
+
+@pytest.mark.parametrize("c,rope,H", WIDTHS + [(512, 64, 16)])
+@pytest.mark.parametrize("rate", [1, 4, 1 << 30, 2 ** 31 - 1])
+def test_last_positions(c, rope, H, rate):
+    """Queries at 2^31 - 1 and just before it: every entry and the whole window, the output rotated back."""
+    s = Setup(c=c, rope=rope, H=H, B=2, N=150, nq=2, n_win=32, seed=c)
+    pos = np.array([2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1 - 40])
+    req = [0, 0, 1, 1]
+    s.check(s.call(pos, rate=rate, q_req=req, rotate=True), pos, rate=rate, q_req=req, rotate=True)
