@@ -428,6 +428,10 @@ typedef struct {
  *   multiplied in bf16; logits, softmax and sums are f32, and the probabilities
  *   enter the second product as the sum of two bf16 terms (within 2^-15 of them), as
  *   does the sum they are divided by.
+ *   Queries that follow one another in a request share its rows on chip where idx
+ *   is NULL, n_heads <= 32, q_req is given and Tq >= 2 * cache->n_req, i.e. where
+ *   a request has several queries on average: for a chunk of a few requests out of
+ *   a large cache give a descriptor of those requests (their rows of the table).
  *   ws: sparse_mqa_attend_fp4_workspace(cfg, Tq, N, n_idx) bytes (n_idx = 0
  *   without idx) for the current device; (size_t)-1 for an unsupported shape. */
 int kv_cache_append(const void* x, int x_is_f32, long long ld_x, int n_rows, const int32_t* row_start,

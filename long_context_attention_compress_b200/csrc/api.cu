@@ -773,6 +773,7 @@ static MqaFp4Problem fp4_problem(const hca_layer_cfg* cfg, int Tq, int N, const 
   p.n_win = cfg->n_win;
   p.Tq = Tq;
   p.H = cfg->n_heads;
+  p.pack = 1;
   p.scale = cfg->scale;
   return p;
 }
@@ -1611,17 +1612,20 @@ int kv_cache_gather(const hca_kv_cache* cache, int B, int n_out, const int32_t* 
 }
 
 // The plan takes a window to be there, so that the size of the workspace does not depend on it.
-static MqaPlan fp4_plan(const hca_layer_cfg* cfg, int Tq, int N, int n_idx, bool q_req) {
+static MqaPlan fp4_plan(const hca_layer_cfg* cfg, int Tq, int N, int n_idx, int pack) {
   MqaFp4Problem p = fp4_problem(cfg, Tq, N, n_idx ? reinterpret_cast<const int32_t*>(1) : nullptr, n_idx,
                                 reinterpret_cast<const hca_bf16*>(1));
-  p.q_req = q_req ? reinterpret_cast<const int32_t*>(1) : nullptr;
+  p.pack = pack;
   return plan_mqa_fp4(p, device_sm_count());
 }
-// Whether the queries name their requests or not.
+// Enough for any number of requests that the queries belong to, named or not.
 static size_t fp4_ws(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
   if (Tq == 0) return 0;
-  const size_t one = fp4_plan(cfg, Tq, N, n_idx, false).ws_bytes;
-  return round256(n_idx || Tq == 1 ? one : std::max(one, fp4_plan(cfg, Tq, N, n_idx, true).ws_bytes));
+  size_t need = fp4_plan(cfg, Tq, N, n_idx, 1).ws_bytes;
+  const int most = n_idx ? 1 : mqa_fp4_pack(cfg->c, cfg->n_heads, Tq, 1);
+  for (int pack = 2; pack <= most; pack = pack < most && 2 * pack > most ? most : 2 * pack)
+    need = std::max(need, fp4_plan(cfg, Tq, N, n_idx, pack).ws_bytes);
+  return round256(need);
 }
 
 size_t sparse_mqa_attend_fp4_workspace(const hca_layer_cfg* cfg, int Tq, int N, int n_idx) {
@@ -1677,7 +1681,8 @@ int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, c
   p.rope_base = cfg->rope_base;
   p.out = reinterpret_cast<bf16*>(out);
   p.check = debug_checks() ? 1 : 0;
-  CUDA_TRY(launch_mqa_fp4(p, fp4_plan(cfg, Tq, N, idx ? n_idx : 0, q_req != nullptr), ws, as_stream(stream)), who);
+  if (q_req && !idx) p.pack = mqa_fp4_pack(cfg->c, cfg->n_heads, Tq, cache->n_req);
+  CUDA_TRY(launch_mqa_fp4(p, fp4_plan(cfg, Tq, N, idx ? n_idx : 0, p.pack), ws, as_stream(stream)), who);
   return HCA_OK;
 }
 

@@ -327,6 +327,7 @@ struct MqaFp4Problem {
   const int32_t* q_pos;
   const int32_t* q_req;     // [Tq] or nullptr: query i belongs to request i
   int Tq, H;
+  int pack;                 // queries that share a CTA's columns (1: none do)
   float scale;
   const float* sink;
   int rope_dims;            // > 0: the output's last rope_dims channels turn back by -q_pos
@@ -334,7 +335,9 @@ struct MqaFp4Problem {
   bf16* out;
   int check;
 };
-// (sizes alone decide the plan: Tq, H, c, N, n_idx and whether idx and win are given)
+// How many queries to let share a CTA: with Tq queries that name their requests, of n_req, and no selection.
+int mqa_fp4_pack(int c, int H, int Tq, long long n_req);
+// (sizes alone decide the plan: Tq, H, c, N, n_idx, pack and whether idx and win are given)
 MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms);
 cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, cudaStream_t stream);
 unsigned int read_and_clear_mqa_fp4_error();  // bit 0: a wait gave up; entry_check bits << 1

@@ -275,8 +275,8 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 // What a CTA attends to.  Without packing: one query and up to 64 of its heads.  Packed (dense entries, at most 32
-// heads, queries that name their requests): the 64 columns of the MMA are the heads of G = 64 / H consecutive queries
-// (32 at most), so that the queries of a chunk share the rows that are widened for them.  The group is cut into runs
+// heads, several queries a request): the 64 columns of the MMA are the heads of G consecutive queries (see mqa_fp4_pack),
+// so that the queries of a chunk share the rows that are widened for them.  The group is cut into runs
 // of neighbouring queries of one request with positions at most kRunStep apart; a run's rows are the union of its
 // queries', and each column masks the rows that its query does not see.
 constexpr int kRunStep = 4;
@@ -948,9 +948,19 @@ __global__ void __launch_bounds__(kThreads, 1) mqa_fp4_tc_kernel(const __grid_co
 extern cudaError_t make_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                                   const uint64_t* strides_bytes, uint32_t box_rows);
 
-// Queries that share a CTA's 64 columns (1: not packed).
-static int packed_queries(const MqaFp4Problem& p) {
-  return p.kv.c == kC && p.q_req && !p.idx && p.H <= kHT / 2 && p.Tq > 1 ? min(32, kHT / p.H) : 1;
+// Queries that share a CTA's 64 columns (1: none do): as many as there are heads' columns for, but no more than a request
+// has queries on average, or a CTA would walk the rows of several requests one after the other.  32 requests of one query
+// each at 8 heads, 1,024 entries: 25 us with one query a CTA, 59 us with eight (measured with P as one term); 192 queries
+// of one request at 16 heads: 58 us with four a CTA, 108 us with two.  A power of two or the most that fit, so that few
+// numbers bound the workspace.
+int mqa_fp4_pack(int c, int H, int Tq, long long n_req) {
+  if (c != kC || H > kHT / 2) return 1;
+  const int most = min(32, kHT / H);
+  const long long each = Tq / max(1ll, n_req);
+  if (each >= most) return most;
+  int pack = 1;
+  while (2 * pack <= each) pack *= 2;
+  return pack;
 }
 
 // Splits per query: fewest tiles on the critical path over whole waves of CTAs (one per SM), a CTA's set-up and
@@ -961,7 +971,7 @@ MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms) {
   pl.max_rows = max(1, entries + window);
   const size_t state = (size_t)p.Tq * p.H * ((size_t)p.kv.c * sizeof(float) + sizeof(float2));
   if (p.kv.c == kC) {
-    const int pack = packed_queries(p);
+    const int pack = p.pack;
     const int tiles = max(1, (entries + kRowsT - 1) / kRowsT + (window + pack - 1 + kRowsT - 1) / kRowsT);
     const long long ctas1 = (long long)((max(1, p.Tq) + pack - 1) / pack) * ((p.H + kHT - 1) / kHT);
     const int smax = (int)min((long long)min(tiles, 1024), max(1ll, 2ll * num_sms / ctas1));
@@ -1012,7 +1022,7 @@ cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, 
   float* ws_o = reinterpret_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)p.Tq * pl.splits * p.H * p.kv.c);
   cudaError_t e;
-  const int pack = packed_queries(p);
+  const int pack = p.pack;
   if (p.kv.c == kC) {
     e = pack > 1 ? launch_tc<true>(p, pack, pl.splits, ws_o, ws_ml, stream)
                  : launch_tc<false>(p, pack, pl.splits, ws_o, ws_ml, stream);

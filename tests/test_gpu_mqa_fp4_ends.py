@@ -119,3 +119,26 @@ def test_last_positions(c, rope, H, rate):
     pos = np.array([2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1 - 40])
     req = [0, 0, 1, 1]
     s.check(s.call(pos, rate=rate, q_req=req, rotate=True), pos, rate=rate, q_req=req, rotate=True)
+
+
+@pytest.mark.parametrize("H", [2, 8, 32])
+def test_one_query_a_request_is_planned_the_same_named_or_not(H):
+    """Queries of different requests have no rows to share: naming the requests changes neither the plan nor a bit."""
+    s = Setup(H=H, B=12, N=700, rpb=32, seed=H)
+    pos = 2700 + 9 * np.arange(12)
+    assert torch.equal(s.call(pos), s.call(pos, q_req=np.arange(12)))
+    req = np.random.default_rng(H).permutation(12)
+    s.check(s.call(pos, q_req=req), pos, q_req=req)
+
+
+def test_chunk_of_one_request_of_a_large_cache():
+    """A handful of queries of one request beside many idle ones, and through a descriptor of that request alone."""
+    import long_context_attention_compress_b200 as hca
+    s = Setup(H=16, B=9, N=300, rpb=32, nq=1, W=140, seed=5)
+    pos, req = 1100 + np.arange(9), np.full(9, 4)
+    s.check(s.call(pos, q_req=req), pos, q_req=req)
+    one = hca.KvCache("fp4", 512, 64, **s.k.t, block_table=s.k.table[4:5].contiguous().cuda())
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    got = hca.sparse_mqa_attend_fp4(s.q.cuda(), one, 300, i32(pos), s.cfg, rate=4, win=s.win[4:5].contiguous().cuda(),
+                                    q_req=i32(np.zeros(9)))
+    s.check(got, pos, q_req=req)
