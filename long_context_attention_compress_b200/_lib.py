@@ -165,13 +165,17 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
-# The current stream's handle without building a torch.cuda.Stream object (3 us a call).
+# The current stream's handle without building a torch.cuda.Stream object (3 us a call), and the current device's number
+# (torch.cuda.current_device() costs three times as much), where this torch has them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _current_device():
-    # (torch.cuda.current_device() costs three times as much; CUDA is up where a tensor lives on it)
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+    # (CUDA is up where a tensor lives on it)
+    if _raw_device is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_device()
+    return _raw_device()
 
 
 def _stream(stream=None, device=None):
