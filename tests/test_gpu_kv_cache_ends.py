@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import oracle
-from kv_cache_util import Cache
-from test_gpu_kv_cache import BASE, FORMS, _check
+from kv_cache_util import Cache, values
+from test_gpu_kv_cache import BASE, FORMS, _check, _ready
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,77 @@ def test_fp8_form_is_one_for_both_calls(dtype):
         same[r, c] = False
     same[7, 64:128] = same[9, 192:256] = False
     assert torch.equal(codes[same], want[same])
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,gamma_on,rotate", [(torch.float32, True, True), (torch.bfloat16, True, True),
+                                                   (torch.float32, True, False), (torch.float32, False, True),
+                                                   (torch.bfloat16, False, False)])
+def test_append_several_rows_a_warp(form, dtype, gamma_on, rotate):
+    """More rows than one a warp (some 3,600 where they are normalised, 5,900 at most): each warp takes a run of them, with
+    the ends of requests and empty requests inside."""
+    import long_context_attention_compress_b200 as hca
+    rng = np.random.default_rng(3)
+    counts = rng.integers(1, 9, 2400)
+    counts[7::11] = 0
+    counts[1200:1204] = [700, 0, 0, 900]
+    B, n, lead = len(counts), int(counts.sum()), 3
+    assert n > 10_000
+    first = rng.integers(0, 20, B)
+    first[50::97] = -1
+    k = Cache(form, 512, 64, B, 28, rpb=4)  # (19 + 8 entries at most)
+    first[1200], first[1203] = -1, 0
+    per = k.table.shape[1]
+    # (of the two long requests one is turned off and one has blocks of its own behind the others')
+    table = torch.cat([k.table, torch.full((B, 240 - per), -1, dtype=torch.int32)], 1)
+    t = {name: torch.cat([v, v[:1].expand(240, *v.shape[1:])]).contiguous() for name, v in k.t.items()}
+    table[1203] = torch.arange(240, dtype=torch.int32) + k.t["codes"].shape[0]
+    k.t, k.table = t, table
+    k.handle = hca.KvCache(form, 512, 64, **t, block_table=table.cuda())
+    x = torch.tensor(rng.normal(size=(lead + n + 5, 512)) * 10.0 ** rng.uniform(-2, 2, size=(lead + n + 5, 1))).to(dtype)
+    start = np.concatenate([[0], np.cumsum(counts)]) + lead
+    gamma = torch.tensor(rng.uniform(0.5, 1.5, 512), dtype=torch.float32) if gamma_on else None
+    before = k.bytes()
+    hca.kv_cache_append(x.cuda(), k.handle, _i32(first), row_start=_i32(start), rate=128,
+                        gamma=None if gamma is None else gamma.cuda(), rotate=rotate, norm_eps=1e-6, rope_base=BASE)
+    on = [(start[b] + j, first[b] + j, b) for b in range(B) if first[b] >= 0 for j in range(counts[b])]
+    src, ent, req = (np.array(v) for v in zip(*on))
+    rows = [k.row(int(b), int(e)) for b, e in zip(req, ent)]
+    _check(k, before, rows, _ready(x[src], ent, 128, None if gamma is None else gamma.cuda(), rotate, 64), rotate)
+
+
+def _random_cache(form, c, rope, B, room, rpb, seed):
+    """A cache of random codes, scales of ordinary size and random rotary channels."""
+    k = Cache(form, c, rope, B, room, rpb=rpb, seed=seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if form == "bf16":
+        k.t["codes"].normal_(generator=g)
+    else:
+        k.t["codes"].random_(0, 127, generator=g)  # (FP8: no NaN)
+        k.t["codes"] += 128 * torch.randint(0, 2, k.t["codes"].shape, generator=g, device="cuda").to(torch.uint8)
+        k.t["scales"].uniform_(0.01, 2.0, generator=g) if form == "fp8" else k.t["scales"].random_(120, 135, generator=g)
+        if rope:
+            k.t["rope"].normal_(generator=g)
+    return k
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("c,rope,n_out,rpb", [(512, 64, 8667, 32), (512, 0, 13001, 0), (128, 0, 40_001, 32), (64, 0, 33_333, 0)])
+def test_gather_several_rounds_a_block(form, c, rope, n_out, rpb):
+    """More rows than the resident blocks take at once (11,840, and 47,360 of at most 128 channels): chosen, consecutive and
+    leading entries, in numbers that end inside a block's round."""
+    import long_context_attention_compress_b200 as hca
+    B, room = 3, n_out + 10
+    k = _random_cache(form, c, rope, B, room, rpb, seed=c + rpb)
+    ref = torch.tensor(values(form, k.bytes(), {n: k.width(n) for n in k.t}, rope)).float().bfloat16()
+    ref = torch.cat([ref, torch.zeros(1, c, dtype=torch.bfloat16)])  # (the last: no row)
+    at = np.array([[k.row(b, e) for e in range(room)] for b in range(B)])
+    rng = np.random.default_rng(1)
+    idx = rng.integers(-3, room, (B, n_out))
+    rows = np.where(idx >= 0, np.take_along_axis(at, np.maximum(idx, 0), 1), -1)
+    got = hca.kv_cache_gather(k.handle, B, n_out, idx=_i32(idx))
+    assert torch.equal(got.cpu(), ref[rows])
+    first = [0, 7, -1]
+    want = [at[0, :n_out], at[1, 7:7 + n_out], np.full(n_out, -1)]
+    assert torch.equal(hca.kv_cache_gather(k.handle, B, n_out, first=_i32(first)).cpu(), ref[np.stack(want)])
+    assert torch.equal(hca.kv_cache_gather(k.handle, B, n_out).cpu(), ref[at[:, :n_out]])
