@@ -85,3 +85,22 @@ def test_weights_of_many_rows_unsplit():
     got = to64(s.call(pos, q_req=np.zeros(320, int)))
     for i in (0, 1, 150, 319):
         held(got[i], to64(s.q[i]), s.rows(i, int(pos[i]), 0, 4, None), what=f"query {i}")
+
+
+@pytest.mark.parametrize("N", [60, 1000])
+def test_split_and_unsplit_queries_agree(N):
+    """A query alone, whose rows go to many CTAs, and among 320, where one CTA walks them: both within the bounds above, so
+    at most a step of bf16 (and twice the f32 bounds) apart, and on few elements."""
+    s = setup(64, N, nq=320, B=1, seed=11)
+    pos = 4 * N + 3 + np.arange(320)
+    many = s.call(pos, q_req=np.zeros(320, int))
+    q = s.q
+    for i in (0, 319):
+        s.q = q[i:i + 1]
+        one = s.call([pos[i]], q_req=[0])
+        rows = s.rows(0, int(pos[i]), 0, 4, None)
+        a, b = to64(one)[0], to64(many)[i]
+        held(a, to64(q[i]), rows, what="split")
+        held(b, to64(q[i]), rows, what="unsplit")
+        keep = np.arange(512) != AT
+        assert np.mean(a[:, keep] != b[:, keep]) <= 0.05
