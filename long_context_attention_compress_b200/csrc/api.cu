@@ -1227,7 +1227,8 @@ int hybrid_attn_decode(const hca_layer_cfg* cfg, const hca_decode_args* a, void*
       p.win_seq_stride = (long long)nw * c;
       p.rope_dims = cfg->rope_dims;
     }
-    return cuda_status(launch_mqa_fp4(p, pl, aws, sm),
+    // (beside the indexer, combine CTAs that wait on its SMs would hold its persistent grid up until they are done)
+    return cuda_status(launch_mqa_fp4(p, pl, aws, sm, sm == st),
                        csa ? "decode: csa attention (fp4)" : "decode: hca attention (fp4)");
   };
   auto run_hca_attention = [&]() -> int {
@@ -1682,7 +1683,7 @@ int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, c
   p.out = reinterpret_cast<bf16*>(out);
   p.check = debug_checks() ? 1 : 0;
   if (q_req && !idx) p.pack = mqa_fp4_pack(cfg->c, cfg->n_heads, Tq, cache->n_req);
-  CUDA_TRY(launch_mqa_fp4(p, fp4_plan(cfg, Tq, N, idx ? n_idx : 0, p.pack), ws, as_stream(stream)), who);
+  CUDA_TRY(launch_mqa_fp4(p, fp4_plan(cfg, Tq, N, idx ? n_idx : 0, p.pack), ws, as_stream(stream), true), who);
   return HCA_OK;
 }
 

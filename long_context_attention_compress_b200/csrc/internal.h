@@ -339,7 +339,8 @@ struct MqaFp4Problem {
 int mqa_fp4_pack(int c, int H, int Tq, long long n_req);
 // (sizes alone decide the plan: Tq, H, c, N, n_idx, pack and whether idx and win are given)
 MqaPlan plan_mqa_fp4(const MqaFp4Problem& p, int num_sms);
-cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, cudaStream_t stream);
+// pdl: the combine's CTAs become resident while the attention runs (not where another stream's kernel wants those SMs)
+cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, cudaStream_t stream, bool pdl);
 unsigned int read_and_clear_mqa_fp4_error();  // bit 0: a wait gave up; entry_check bits << 1
 
 // ---- mqa_tc.cu (tcgen05) -------------------------------------------------------------

@@ -1017,7 +1017,7 @@ static cudaError_t launch_tc(const MqaFp4Problem& p, int pack, int splits, float
   return cudaGetLastError();
 }
 
-cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, cudaStream_t stream) {
+cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, cudaStream_t stream, bool pdl) {
   if (p.Tq == 0) return cudaSuccess;
   float* ws_o = reinterpret_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)p.Tq * pl.splits * p.H * p.kv.c);
@@ -1036,7 +1036,7 @@ cudaError_t launch_mqa_fp4(const MqaFp4Problem& p, const MqaPlan& pl, void* ws, 
   ++g_launch_counter;
   if (p.kv.c == kC && pack == 1 && pl.splits == 1) return cudaSuccess;
   return launch_mqa_combine(ws_o, ws_ml, p.Tq, pl.splits, p.H, p.kv.c, p.out, p.sink, p.q_pos, p.rope_dims, p.rope_base,
-                            stream, true);
+                            stream, pdl);
 }
 
 unsigned int read_and_clear_mqa_fp4_error() {

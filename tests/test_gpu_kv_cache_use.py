@@ -82,3 +82,39 @@ def test_newest_entry_of_the_layer_call(rpb, norm):
     assert step.max() <= 1 and np.mean(step > 0) <= (1 / 30 if norm else 1 / 100), (step.max(), np.mean(step > 0))
     rope = to64(torch.tensor(have["rope"]).view(torch.bfloat16))
     assert np.all(np.abs(rope - new[:, 448:]) <= 2.0 ** -7 * np.abs(new[:, 448:]) + 1e-6)
+
+
+def test_fp4_hca_cache_runs_beside_the_indexer():
+    """The hybrid decode step of 8 requests at 1M tokens with an FP4 HCA cache: its attention overlaps the indexer as the
+    bf16 one does (one after the other the step took 1.63 times as long; a fifth is allowed for noise)."""
+    import long_context_attention_compress_b200 as hca
+    s = wl.PRO
+    cfg = hca.make_cfg(s)
+    B, ctx = 8, 1 << 20
+    d = wl.hybrid_decode_inputs(s, B, ctx, seed=1, device="cuda")
+    Nh = d["hca"]["E_h"].shape[1]
+    t = {"codes": torch.empty(B, Nh, 224, dtype=torch.uint8, device="cuda"),
+         "scales": torch.empty(B, Nh, 16, dtype=torch.uint8, device="cuda"),
+         "rope": torch.empty(B, Nh, 64, dtype=torch.bfloat16, device="cuda")}
+    k = hca.KvCache("fp4", s.c, 64, **t)
+    hca.kv_cache_append(d["hca"]["E_h"].reshape(B * Nh, s.c), k, _i32([0] * B), row_start=_i32(np.arange(B + 1) * Nh))
+    idx = torch.empty((B, s.topk), dtype=torch.int32, device="cuda")
+    oc = torch.empty((B, s.n_heads, s.c), dtype=torch.bfloat16, device="cuda")
+    oh = torch.empty_like(oc)
+    calls = []
+    for gh, kw in ((d["hca"], {}), ({n: v for n, v in d["hca"].items() if n != "E_h"} | {"N": Nh}, {"hca_kv4": k})):
+        args, keep = hca.make_decode_args(B, d["csa"]["q_pos"], csa=d["csa"], hca=gh, csa_topk_idx=idx, csa_out=oc,
+                                          hca_out=oh, **kw)
+        ws = torch.empty((hca.hybrid_attn_decode_workspace(cfg, args),), dtype=torch.uint8, device="cuda")
+        calls.append((args, keep, ws))
+    times = ([], [])
+    for i in range(60):
+        args, _, ws = calls[i % 2]
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        hca.hybrid_attn_decode(cfg, args, ws=ws)
+        b.record()
+        torch.cuda.synchronize()
+        times[i % 2].append(a.elapsed_time(b))
+    bf16, fp4 = (float(np.median(v[5:])) for v in times)
+    assert fp4 <= 1.2 * bf16, (bf16, fp4)
