@@ -117,10 +117,9 @@ __device__ __forceinline__ int mx_exponent(float amax) {
 constexpr int kFp8Group = 64;
 constexpr double kE4m3Max = 448.0;
 
-// E4M3 byte of q (f64), ties to even, saturating, a NaN kept; sign bit 7, exponent bits 3-6
+// E4M3 byte of q (f64; a NaN gives 0), ties to even, saturating; sign bit 7, exponent bits 3-6
 // (bias 7, field 0 = subnormal with spacing 2^-9), mantissa bits 0-2.
 __device__ __forceinline__ uint32_t e4m3_encode(double q) {
-  if (q != q) return 0x7Fu;  // NaN
   const uint32_t sign = q < 0.0 ? 0x80u : 0u;
   const double a = fabs(q);
   if (a >= kE4m3Max) return sign | 0x7Eu;  // 1.75 * 2^8 = 448
@@ -139,7 +138,7 @@ __device__ __forceinline__ uint32_t e4m3_encode(double q) {
     m = 8;
     ++e;
   }
-  if (m < 8) return sign | (uint32_t)m;  // subnormal (e = -6): exponent field 0
+  if (m < 8) return sign | ((uint32_t)m & 7u);  // subnormal (e = -6): exponent field 0
   return sign | ((uint32_t)(e + 7) << 3) | (uint32_t)(m - 8);
 }
 

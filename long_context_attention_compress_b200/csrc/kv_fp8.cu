@@ -35,6 +35,22 @@ __device__ __forceinline__ float load_x(const void* x, long long i) {
   return __bfloat162float(reinterpret_cast<const bf16*>(x)[i]);
 }
 
+// A group with values that are not finite (rare, so calls): its largest magnitude that is not a NaN, and the code of NaN
+// where x / scale is one (a NaN, or an infinity, whose group's scale is infinite).
+template <bool F32>
+__device__ __noinline__ float group_max(const void* x, long long at) {
+  float m = 0.f;
+  for (int j = 0; j < kFp8Group; ++j) m = fmaxf(m, fabsf(load_x<F32>(x, at + j)));
+  return m;
+}
+template <bool F32>
+__device__ __noinline__ void mark_nans(const void* x, long long at, double scale, uint8_t* codes) {
+  for (int j = 0; j < kFp8Group; ++j) {
+    const double q = (double)load_x<F32>(x, at + j) / scale;
+    if (q != q) codes[j] = 0x7F;
+  }
+}
+
 // One thread per 64-channel group of the FP8 part, or per 8 rotary channels.
 template <bool F32>
 __global__ void __launch_bounds__(256) kv_fp8_quantize_kernel(const void* __restrict__ x, long long ld_x, long long rows,
@@ -57,10 +73,12 @@ __global__ void __launch_bounds__(256) kv_fp8_quantize_kernel(const void* __rest
     return;
   }
   const int j0 = u * kFp8Group;
-  float amax = 0.f;
-  for (int j = 0; j < kFp8Group; ++j) amax = fmaxf(amax, fabsf(load_x<F32>(x, xr + j0 + j)));
+  uint32_t top = 0u;  // as bits, where infinities and NaN come after the finite values
+  for (int j = 0; j < kFp8Group; ++j) top = max(top, __float_as_uint(load_x<F32>(x, xr + j0 + j)) & 0x7fffffffu);
+  const bool finite = top < 0x7f800000u;
+  const float amax = finite ? __uint_as_float(top) : group_max<F32>(x, xr + j0);
   const float sc = amax > 0.f ? __double2float_rn((double)amax / kE4m3Max) : 1.f;
-  const double sd = (double)sc;
+  const double sd = sc > 0.f ? (double)sc : 1e-300;  // (a scale that rounded to 0: the largest code, and 0 for zeros)
   uint8_t* cp = codes + r * ld_codes + j0;
   for (int j = 0; j < kFp8Group; j += 16) {
     uint32_t w[4];
@@ -68,14 +86,12 @@ __global__ void __launch_bounds__(256) kv_fp8_quantize_kernel(const void* __rest
     for (int k = 0; k < 4; ++k) {
       uint32_t word = 0;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float v = load_x<F32>(x, xr + j0 + j + 4 * k + b);
-        if (v != 0.f) word |= e4m3_encode((double)v / sd) << (8 * b);  // (a group's scale may have rounded to 0)
-      }
+      for (int b = 0; b < 4; ++b) word |= e4m3_encode((double)load_x<F32>(x, xr + j0 + j + 4 * k + b) / sd) << (8 * b);
       w[k] = word;
     }
     *reinterpret_cast<uint4*>(cp + j) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  if (!finite) mark_nans<F32>(x, xr + j0, sd, cp);
   scales[r * ld_scales + u] = sc;
 }
 
