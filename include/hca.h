@@ -349,8 +349,8 @@ int sparse_mqa_attend(const hca_bf16* q, const hca_bf16* kv, long long kv_seq_st
  *                positive multiple of 32).  A row is 366 bytes at c = 512 with
  *                64 rotary channels.  A scale byte is at most 254.
  * FP8 keeps a NaN, and an infinity makes its group's 64 channels NaN.  FP4 has
- * no code for either: a NaN is taken for the largest magnitude of its group, and
- * an infinity's group reads back as infinities and zeros.
+ * no code for either: a NaN reads back as 6 * 2^X of its group (the largest value
+ * there), and an infinity's group as infinities and zeros.
  * ld_codes is in bf16 elements (BF16) or bytes, ld_scales in f32 (FP8) or bytes
  * (FP4), ld_rope in bf16 elements.  Rows of codes and of rope start on 16-byte
  * boundaries.  c is a multiple of 8, at most 512; rope_dims a multiple of 8,
@@ -396,13 +396,14 @@ typedef struct {
  *   compressed entries (rms_norm_rope's convention).
  *   gamma [c] f32 or NULL: RMSNorm with norm_eps; rotate nonzero: the last
  *   rope_dims channels turn by their position with base rope_base.  With either,
- *   the stored form is that of the value rounded to bf16, i.e. the cache holds
- *   what rms_norm_rope followed by kv_fp8_quantize or mxfp4_quantize gives;
- *   with neither, that of x.  n_rows <= 2^30.  x does not overlap the cache; two requests of one
- *   call do not name the same row (a block shared by their tables is appended to
- *   by one of them at most).
+ *   the stored form is that of the float64 value rounded to f32 and to bf16, i.e.
+ *   the cache holds what rms_norm_rope followed by kv_fp8_quantize or
+ *   mxfp4_quantize gives (where the products of rms_norm_rope, which are f32, stay
+ *   in f32's normal range); with neither, that of x.  n_rows <= 2^30.  x does not
+ *   overlap the cache; two requests of one call do not name the same row (a block
+ *   shared by their tables is appended to by one of them at most).
  *
- * kv_cache_gather -- rows of a cache as bf16 (code * scale, rounded once):
+ * kv_cache_gather -- rows of a cache as bf16 (code * scale in f32, then rounded):
  *   out[b*seq_stride_out + j*ld_out ..] for b < B <= n_req, j < n_out is request
  *   b's entry idx[b][j] (idx [B][n_out] int32), or first[b] + j, or j with both
  *   NULL.  A negative entry, a negative first[b] and an entry without a row give
@@ -424,10 +425,10 @@ typedef struct {
  *   read.  c is a multiple of 32; scales are 16-byte aligned and ld_scales a
  *   multiple of 16; n_idx <= 4096, Tq and n_win <= 2^20, N <= 2^30, and the cache
  *   has fewer than 2^31 rows.  out overlaps no input.  A row that is not finite
- *   reaches the queries that see it and no other.  The entries are widened on chip (exactly) and
- *   multiplied in bf16; logits, softmax and sums are f32, and the probabilities
- *   enter the second product as the sum of two bf16 terms (within 2^-15 of them), as
- *   does the sum they are divided by.
+ *   reaches the queries that see it and no other.  The entries are widened on chip
+ *   (exactly) and multiplied in bf16; logits, softmax and sums are f32, and the
+ *   probabilities enter the second product as the sum of two bf16 terms (within
+ *   2^-15 of them), as does the sum they are divided by.
  *   Queries that follow one another in a request share its rows on chip where idx
  *   is NULL, n_heads <= 32, q_req is given and Tq >= 2 * cache->n_req, i.e. where
  *   a request has several queries on average: for a chunk of a few requests out of

@@ -8,25 +8,27 @@
 // (FP8) shuffles away and nothing passes through memory between the input and the stored row; rows of at most 128
 // channels that are only converted take half a warp.  The next row's load is always under way.
 // Roundings.  With normalisation or rotation y is rounded to bf16 first (what the bf16 cache holds), as from the
-// float64 value: a quantised code must not depend on which side of a midpoint an f32 normalisation falls.  Sum of
+// float64 value (by way of f32): a quantised code must not depend on which side of a midpoint an f32 normalisation falls.  Sum of
 // squares and rotation are f64; the other channels are formed in f32, 8 ulps too low and too high (f32 is within 4),
 // and redone in f64 only where the two round apart, or where a factor or a product may leave f32's normal range.  The codes are those of the stored-form definitions bit for bit:
 // FP4 scaling is exact and the conversion rounds to nearest even; an f32 quotient (by the reciprocal, within 2 ulps)
 // that is within 4 ulps of an E4M3 midpoint, or in E4M3's subnormal range, is decided on the f64 quotient.
 // The angle is formed in turns from theta / 2 pi in two f64 words (a table made on the host) with an error-free product,
 // so that its fraction is good to 2^-52 at any position and the sine and cosine need no long reduction.
-// Bound: by HBM only where rows are converted as they are (c*4 B in, 366 B out for FP4 at c = 512); with normalisation
-// and rotation by issue slots, 760 instructions a row at 0.6 a cycle and scheduler.  Measured, c = 512: 16,384 f32 rows
-// normalised to FP4 19.1 us (6.0 us of HBM time; 7.5 us for the loads alone), 3,001 to FP8 in 13 ragged requests 7.4 us,
-// 256 bf16 rows into rings 2.1 us, 8 rows 4.0 us: a row's chain of loads, f64 sum, inverse root and sine.  An f32
-// normalisation with error bounds and f64 behind it for every fifth row took 2 us longer for the 16,384.
+// Bound: rows converted as they are, by the chain request, first entry, block table, store and by issue slots (24,577 FP4
+// rows of 128 channels 5.3 us, 1.2 us of HBM time, 55 % of the slots taken); with normalisation and rotation by issue slots, 740 instructions a row at 0.6 a cycle and scheduler.  Measured, c = 512: 16,384 f32 rows
+// normalised to FP4 19.3 us (6.0 us of HBM time; 7.5 us for the loads alone), 3,001 to FP8 in 13 ragged requests 7.4 us
+// and 4,100 bf16 rows 6.5 us (a row or two a warp), 256 bf16 rows into rings 2.1 us, 8 rows 4.0 us: a row's chain of
+// loads, f64 sum, inverse root and sine.  An f32 normalisation with error bounds and f64 behind it for every fifth row
+// took 2 us longer for the 16,384.
 //
 // kv_gather_kernel.  The bf16 values of rows.  Each row is a chain of dependent loads (index, block table, row): a block
 // resolves 16 rows at a time, one a thread, while its warps move the 16 before, two rows in flight per warp (their
 // loads predicated, not branched around, so that they issue together); rows of at most 128 channels take half a warp,
-// four in flight (24,577 rows of 128 FP4 channels 4.0 us, a warp a row 6.3).  Bound by memory: 8 x 8,191 FP4 rows 18.3 us
-// (5.0 TB/s read and written; 13.9 us at the copy rate), 32 x 1,024 selected FP8 rows 10.3 us (5.2 TB/s); with four rows
-// a warp and three blocks an SM 18.9 and 10.7, with two and six 18.5 and 11.4.
+// four in flight (24,577 rows of 128 FP4 channels 4.0 us, a warp a row 6.3).  bf16 rows move at the copy rate (8 x 8,191
+// in 20.2 us); rows that are widened are bound by issue slots (two thirds of them taken, the ALU at 62 %, DRAM at 1.6 TB/s
+// while the output stays in L2): 8 x 8,191 FP4 rows 18.5 us (13.9 at the copy rate), 32 x 1,024 selected FP8 rows 10.6 us
+// (8.2); with four rows a warp and three blocks an SM 18.9 and 10.7, with two and six 18.5 and 11.4.
 
 #include <cuda_fp16.h>
 
@@ -119,7 +121,7 @@ __device__ __forceinline__ uint2 e4m3x8_encode(const float* y, float sc) {
   return r;
 }
 
-// Two f32 products in one instruction (16,384 normalised rows 19.7 -> 19.1 us).
+// Two f32 products in one instruction (16,384 normalised rows 0.6 us faster).
 __device__ __forceinline__ float2 mul2(float a0, float a1, float b0, float b1) {
   float2 r;
   asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
@@ -137,8 +139,8 @@ struct NoTurns {};  // (a launch that only converts does not carry the table)
 template <bool XF>
 using TurnsOf = std::conditional_t<XF, Turns, NoTurns>;
 
-// Resident blocks per SM that the registers are held to.  Normalised, bf16 form: 7 against 6 took 6.3 against 6.9 us for
-// 4,100 rows; FP8 and FP4, which need a few registers more: 6 against 7 took 25.7 against 26.1 us for 16,384 FP4 rows and
+// Resident blocks per SM that the registers are held to.  Normalised, bf16 form: 7 against 6 took 6.4 against 6.8 us for
+// 4,100 rows; FP8 and FP4, which need a few registers more: 6 against 7 took 24.9 against 25.3 us for 16,384 FP4 rows and
 // their read-back.
 constexpr int append_blocks(int form, bool xf) {
   return xf ? (form == HCA_KV_BF16 ? 7 : 6) : form == HCA_KV_FP8 ? 8 : 10;

@@ -69,7 +69,7 @@ __device__ __forceinline__ const bf16* window_row(const MqaFp4Problem& p, const 
 // ---- CUDA cores: c other than 512 ------------------------------------------------------
 // One CTA per (query, group of kSH heads, split): rows are widened into shared memory 16 at a time, an online softmax
 // runs over them, and the state (m, l, o) goes to the combine kernel.  Bound by f32 FMAs and shared memory: it took
-// 1.2 ms for the 8 x 8,192 entries of c = 512 that take 37.0 us below; the small widths it serves are short.
+// 1.2 ms for the 8 x 8,192 entries of c = 512 that take 37.3 us below; the small widths it serves are short.
 constexpr int kSThreads = 256, kSRows = 16, kSH = 4;
 
 __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem p, int splits, int rows_per_split,
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kSThreads) mqa_fp4_simple_kernel(MqaFp4Problem
 //                 brought to L2 a tile ahead), window rows are copied with 16-byte cp.async
 // Where few heads would leave columns empty, they are given to neighbouring queries (see Group below).
 //
-// Measured at 64 heads: 8 requests x 8,192 entries 37.0 us, 32 x 1,024 selected 31.9 us; 16 heads, 2 x 192 queries over
+// Measured at 64 heads: 8 requests x 8,192 entries 37.3 us, 32 x 1,024 selected 31.8 us; 16 heads, 2 x 192 queries over
 // 2,900 entries 113 us.  With P as one bf16 term they took 33.6, 29.3 and 101 us, and the outputs were off by a third
 // more than their own rounding.  Steady state, every SM at work: 8.8 k cycles a tile (7.3 k with one term): the softmax,
 // then PV (2.3 k: 288 KiB of operands at the shared-memory rate), the blocks' refill (128 KiB of stores) beside PV's end
