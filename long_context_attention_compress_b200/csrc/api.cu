@@ -1648,7 +1648,9 @@ int sparse_mqa_attend_fp4(const hca_bf16* q, const hca_kv_cache* cache, int N, c
   if ((s = check_kv4(cfg, cache, 0, who)) != HCA_OK) return s;
   CHECK(Tq >= 0 && Tq <= kMaxFp4Queries && N >= 0 && N <= kMaxFp4Entries && rate >= 1, HCA_ERR_INVALID_ARG,
         "%s: Tq=%d (at most %d) N=%d (at most %d) rate=%d", who, Tq, kMaxFp4Queries, N, kMaxFp4Entries, rate);
-  CHECK(idx ? (n_idx > 0 && n_idx <= 4096) : n_idx == 0, HCA_ERR_INVALID_ARG, "%s: n_idx=%d", who, n_idx);
+  // (an empty batch has no index array, whatever its width)
+  CHECK(idx ? (n_idx > 0 && n_idx <= 4096) : (n_idx == 0 || (Tq == 0 && n_idx > 0)), HCA_ERR_INVALID_ARG, "%s: n_idx=%d",
+        who, n_idx);
   CHECK(q_req || Tq <= cache->n_req, HCA_ERR_INVALID_ARG, "%s: %d queries for %d requests without q_req", who, Tq,
         cache->n_req);
   CHECK(!win || (win_rows >= cfg->n_win && win_seq_stride >= 0 && win_seq_stride % 8 == 0 &&
