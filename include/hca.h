@@ -395,13 +395,14 @@ typedef struct {
  *   Entry e sits at position (e+1)*rate - 1: rate 1 for raw tokens, m or m' for
  *   compressed entries (rms_norm_rope's convention).
  *   gamma [c] f32 or NULL: RMSNorm with norm_eps; rotate nonzero: the last
- *   rope_dims channels turn by their position with base rope_base.  With either,
- *   the stored form is that of the float64 value rounded to f32 and to bf16, i.e.
- *   the cache holds what rms_norm_rope followed by kv_fp8_quantize or
- *   mxfp4_quantize gives (where the products of rms_norm_rope, which are f32, stay
- *   in f32's normal range); with neither, that of x.  n_rows <= 2^30.  x does not
- *   overlap the cache; two requests of one call do not name the same row (a block
- *   shared by their tables is appended to by one of them at most).
+ *   rope_dims channels (if any) turn by their position with base rope_base.  With
+ *   gamma or channels that turn, the stored form is that of the float64 value
+ *   rounded to f32 and to bf16, i.e. the cache holds what rms_norm_rope followed by
+ *   kv_fp8_quantize or mxfp4_quantize gives (where the products of rms_norm_rope,
+ *   which are f32, stay in f32's normal range); with neither, that of x.
+ *   n_rows <= 2^30.  x does not overlap the cache; two requests of one call do not
+ *   name the same row (a block shared by their tables is appended to by one of them
+ *   at most).
  *
  * kv_cache_gather -- rows of a cache as bf16 (code * scale in f32, then rounded):
  *   out[b*seq_stride_out + j*ld_out ..] for b < B <= n_req, j < n_out is request
